@@ -18,7 +18,8 @@
  * with silu(x) = x * sigmoid(x). No softmax, no 1/sqrt(d) score scale.
  * Sections below: the attention; the layer around it (projections, the
  * input and output LayerNorms, the whole layer); row-wise E4M3 (FP8)
- * projections; the attention backward (bf16 on tensor cores, and fp32).
+ * projections; the attention backward (bf16 on tensor cores, and fp32);
+ * serving (a paged key/value cache, the attention over it, 4-bit weights).
  *
  * Conventions for every entry point:
  *  - Pointers marked "device" must be device memory of the current CUDA device
@@ -396,6 +397,136 @@ hstu_status_t hstu_attn_bwd(hstu_dtype_t dtype, const void* q, int64_t q_stride,
                             int32_t num_time_buckets, int32_t max_seqlen, float* dq, float* dk,
                             float* dv, float* dpos, float* dtime, void* workspace,
                             size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------- serving */
+
+/* New tokens over a paged key/value cache. The reference's pages say of cached
+ * incremental decoding that it is not included (generative-recommenders
+ * README, the DLRM-v3 section); the semantics here follow from the attention
+ * above, restricted to the rows of the new tokens.
+ *
+ * A cache is k_cache and v_cache of num_pages pages with page_size tokens each
+ * (a power of two, 16..1024; num_pages * page_size <= 2^31 - 1): device
+ * tensors [num_pages, page_size, H, d] with a page stride and a token stride in
+ * elements (heads contiguous in a token), so both may be views of one
+ * allocation; and ts_cache, int64 [num_pages, page_size] with a page stride,
+ * where the time-bucket term is used. Token p of sequence b lies in page
+ * block_table[b][p / page_size], row p % page_size; slot = page * page_size +
+ * row. block_table: device int32 [B, max_pages], row stride table_stride.
+ *
+ * A step gives sequence b, which has ctx_lens[b] tokens in the cache (device
+ * int32 [B]), the new tokens new_offsets[b] .. new_offsets[b+1]-1 of the
+ * step's packed [total_new, ...] tensors (device int64 [B+1], from 0 to
+ * total_new). They stand at positions ctx_lens[b], ctx_lens[b] + 1, ... of the
+ * cache. In order: hstu_cache_plan (which pages), hstu_cache_append (their keys
+ * and values), hstu_attn_cached_fwd. */
+
+/* Block tables and slots of a step, one launch. Sequence b holds the first
+ * ceil(ctx_lens[b] / page_size) entries of its table row already; the entries
+ * behind them, up to what ctx_lens[b] + its new tokens need, are taken in
+ * sequence order from free_pages (device int32 [num_free]), starting at index
+ * *free_start (device int32), and written to its row; *free_end (device int32)
+ * gets the index of the first page not taken. slots (device int64 [total_new])
+ * gets every new token's slot. Entries behind a sequence's last page are left
+ * as they are. Where the list is short, the missing entries and the slots in
+ * them are -1 and *free_end is num_free; a sequence with impossible numbers
+ * (negative lengths, more than max_pages pages, offsets that decrease) takes no
+ * pages, its slots are -1; both report HSTU_ERR_BAD_INPUT. free_end must not
+ * be free_start. */
+hstu_status_t hstu_cache_plan(const int32_t* ctx_lens, const int64_t* new_offsets, int32_t B,
+                              int64_t total_new, int32_t page_size, const int32_t* free_pages,
+                              int32_t num_free, const int32_t* free_start, int32_t* block_table,
+                              int64_t table_stride, int32_t max_pages, int64_t* slots,
+                              int32_t* free_end, void* stream);
+
+/* Copies the rows of k [total_new, H, d_qk] and v [total_new, H, d_v] (token
+ * strides in elements) and, where given (both or neither), the timestamps
+ * (device int64 [total_new]) to their slots. A negative slot is a padded row
+ * and is skipped; one past the cache is skipped and reports
+ * HSTU_ERR_BAD_INPUT. Slots of one call must differ: which of two rows stays in
+ * a slot named twice is not specified. bf16 or fp32, any alignment of the
+ * element type (16-byte aligned rows are copied 16 bytes at a time). One
+ * launch. */
+hstu_status_t hstu_cache_append(hstu_dtype_t dtype, const void* k, int64_t k_stride, const void* v,
+                                int64_t v_stride, const int64_t* timestamps, const int64_t* slots,
+                                int64_t total_new, int32_t H, int32_t d_qk, int32_t d_v,
+                                void* k_cache, int64_t k_page_stride, int64_t k_tok_stride,
+                                void* v_cache, int64_t v_page_stride, int64_t v_tok_stride,
+                                int64_t* ts_cache, int64_t ts_page_stride, int32_t num_pages,
+                                int32_t page_size, void* stream);
+
+/* Attention of the new tokens over the cache, which holds the context and the
+ * new tokens themselves. parents (device int32 [total_new], or NULL) makes each
+ * sequence's new tokens a tree: parents[i] is the index, within the sequence's
+ * new tokens, of the one that token i follows (smaller than i), or -1 where it
+ * follows the context. NULL: a chain, each token follows the one before.
+ * Candidates that are scored side by side all have parent -1. New token i sees
+ * the whole context, its ancestors and itself, and stands at position p_i =
+ * ctx_lens[b] + (number of its ancestors); a cached token's position is its
+ * index. With that
+ *   s_ij = <q_i, k_j> + pos_bias[h][min(p_i - p_j, num_pos - 1)]
+ *          + time_bias[h][clamp(floor(log2(max(1, ts_i - ts_j))), 0, NB - 1)]
+ *   out_i = (1 / max_seqlen) * sum_{j seen by i} silu(s_ij) v_j
+ * so a chain gives the rows that hstu_attn_fwd gives for these tokens of the
+ * whole sequence. What lies in the cache outside a sequence's tokens, and the
+ * values of tokens that a query does not see, do not matter (they may be NaN).
+ *   q : device [total_new, H, d_qk] of `dtype`, out : [total_new, H, d_v]; the
+ *       rows of every sequence's new tokens are written, nothing else is
+ *   max_new : the most new tokens a sequence has (>= 1; at most 256 with
+ *       parents); max_seqlen : N, and the most tokens a sequence has
+ *   timestamps : the new tokens', device int64 [total_new]; the time term is
+ *       dropped unless timestamps, ts_cache and time_bias are all given
+ *   workspace : device, 16-byte aligned, hstu_attn_cached_workspace_bytes(
+ *       dtype, max_new, d_v) bytes; needs no preparation, holds nothing
+ *       between calls; calls that may overlap need one each
+ * Supported: bf16 with d_qk == d_v in {32, 64, 128} (bases 16-byte aligned,
+ * strides multiples of 8); fp32 with d_qk, d_v <= 128. A sequence with
+ * impossible numbers (longer than max_seqlen or its table row, more new tokens
+ * than max_new) is left out, a page outside the cache counts as no tokens, a
+ * parent that is not before its token counts as -1; all report
+ * HSTU_ERR_BAD_INPUT. Results are the same bits on every run. Two launches. */
+size_t hstu_attn_cached_workspace_bytes(hstu_dtype_t dtype, int32_t max_new, int32_t d_v);
+hstu_status_t hstu_attn_cached_fwd(hstu_dtype_t dtype, const void* q, int64_t q_tok_stride,
+                                   const void* k_cache, int64_t k_page_stride,
+                                   int64_t k_tok_stride, const void* v_cache,
+                                   int64_t v_page_stride, int64_t v_tok_stride,
+                                   const int64_t* ts_cache, int64_t ts_page_stride,
+                                   int32_t num_pages, int32_t page_size,
+                                   const int32_t* block_table, int64_t table_stride,
+                                   int32_t max_pages, const int32_t* ctx_lens,
+                                   const int64_t* new_offsets, int32_t B, int64_t total_new,
+                                   int32_t max_new, int32_t H, int32_t d_qk, int32_t d_v,
+                                   const int64_t* timestamps, const int32_t* parents,
+                                   const float* pos_bias, int32_t num_pos, const float* time_bias,
+                                   int32_t num_time_buckets, int32_t max_seqlen, void* out,
+                                   int64_t out_tok_stride, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/* 4-bit weights with group scales. For each group of `group` (32, 64 or 128)
+ * consecutive weights of a row of W (device bf16 [N, K], row stride ldw):
+ *   scale = bf16(max |w| / 7),  code = clamp(rint(w / scale), -8, 7) + 8,
+ * so w ~ (code - 8) * scale. codes: device uint8 [N, K/2], row stride ldc; byte
+ * k/2 holds the code of the even k in its low four bits. scales: device bf16
+ * [N, K/group], row stride lds. A group of zeros (or whose scale rounds to
+ * zero) gets codes 8 and scale 1; a group with a weight that is not finite gets
+ * scale NaN. K % group == 0. One launch. */
+hstu_status_t hstu_quant_groups_w4(const void* W, int64_t ldw, int64_t N, int32_t K, int32_t group,
+                                   void* codes, int64_t ldc, void* scales, int64_t lds,
+                                   void* stream);
+
+/* y[M, N] = epilogue(x[M, K] ((code - 8) scale)[N, K]^T + bias[N]): the
+ * projections of a few rows (single tokens up to small batches), bound by the
+ * weights' bytes. Codes and scales as hstu_quant_groups_w4 writes them; x, y,
+ * residual bf16, bias fp32 [N] or NULL, epilogues as hstu_linear_fwd. Products
+ * are exact in fp32 before the scale, sums are fp32, and the result is rounded
+ * once. K % 128 == 0, any N >= 1; x and codes 16-byte aligned, ldx % 8 == 0,
+ * ldc % 16 == 0. For many rows hstu_linear_fwd and hstu_linear_fp8_fwd are the
+ * faster calls: the weights are read once for every 64 rows. */
+hstu_status_t hstu_linear_w4_fwd(const void* x, int64_t ldx, int64_t M, int32_t K, const void* codes,
+                                 int64_t ldc, const void* scales, int64_t lds, int32_t group,
+                                 int32_t N, const float* bias, hstu_epilogue_t epilogue,
+                                 const void* residual, int64_t ldr, void* y, int64_t ldy,
+                                 void* stream);
 
 #ifdef __cplusplus
 }

@@ -59,6 +59,21 @@ SIGNATURES = {
     "hstu_layer_fp8_fwd": (ctypes.c_int, [c_p, c_i64, c_i32, c_p, c_p, c_p, c_p, c_p, c_p, c_p,
                                           c_p, c_f32, c_i32, c_p, c_p, c_p, c_i32, c_i32, c_i32,
                                           c_p, c_p, c_i32, c_p, c_i32, c_i32, c_p, c_p, c_sz, c_p]),
+    "hstu_cache_plan": (ctypes.c_int, [c_p, c_p, c_i32, c_i64, c_i32, c_p, c_i32, c_p, c_p, c_i64,
+                                       c_i32, c_p, c_p, c_p]),
+    "hstu_cache_append": (ctypes.c_int, [ctypes.c_int, c_p, c_i64, c_p, c_i64, c_p, c_p, c_i64,
+                                         c_i32, c_i32, c_i32, c_p, c_i64, c_i64, c_p, c_i64, c_i64,
+                                         c_p, c_i64, c_i32, c_i32, c_p]),
+    "hstu_attn_cached_workspace_bytes": (c_sz, [ctypes.c_int, c_i32, c_i32]),
+    "hstu_attn_cached_fwd": (ctypes.c_int, [ctypes.c_int, c_p, c_i64, c_p, c_i64, c_i64, c_p,
+                                            c_i64, c_i64, c_p, c_i64, c_i32, c_i32, c_p, c_i64,
+                                            c_i32, c_p, c_p, c_i32, c_i64, c_i32, c_i32, c_i32,
+                                            c_i32, c_p, c_p, c_p, c_i32, c_p, c_i32, c_i32, c_p,
+                                            c_i64, c_p, c_sz, c_p]),
+    "hstu_quant_groups_w4": (ctypes.c_int, [c_p, c_i64, c_i64, c_i32, c_i32, c_p, c_i64, c_p,
+                                            c_i64, c_p]),
+    "hstu_linear_w4_fwd": (ctypes.c_int, [c_p, c_i64, c_i64, c_i32, c_p, c_i64, c_p, c_i64, c_i32,
+                                          c_i32, c_p, ctypes.c_int, c_p, c_i64, c_p, c_i64, c_p]),
 }
 
 HSTU_OK, HSTU_ERR_INVALID_ARG, HSTU_ERR_UNSUPPORTED, HSTU_ERR_CUDA, HSTU_ERR_TIMEOUT, \

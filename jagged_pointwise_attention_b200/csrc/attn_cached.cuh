@@ -1,0 +1,269 @@
+// attn_cached.cuh -- attention of new tokens over a paged cache: the work
+// line, the tree of new tokens and the join, shared by the bf16 and the fp32
+// kernel.
+//
+//   out_i = (1/N) sum_{j seen by i} silu(q_i.k_j + pos[p_i - p_j]
+//                                        + time[bucket(t_i - t_j)]) v_j
+// A sequence has ctx cached tokens and n new ones, whose keys and values lie
+// in the cache at positions ctx .. ctx + n - 1. New token i sees the cached
+// tokens, its ancestors among the new ones, and itself; p is ctx + depth for
+// new tokens, the index for cached ones.
+//
+// Work line. An item is (sequence, query tile of NQ new tokens, head); it has
+// ceil(len / KT) key tiles, len = ctx + min(n, (qt + 1) NQ) (no new token sees
+// a later one). The key tiles of all items, in that order, form one line, and
+// block c of the grid takes an equal, contiguous part of it, so long and short
+// sequences and any batch load all blocks alike. There is no softmax, so an
+// item that several blocks share is their plain sum: each writes its part (32
+// bits) to the workspace and a second, small launch adds the parts in line
+// order -- no atomics, the same bits on every run. Every block finds its part
+// by itself: a scan over the B sequence lengths, which costs it about a
+// microsecond and saves a planning launch.
+#pragma once
+
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace hstu {
+
+constexpr int kMaxTree = 256;       // new tokens of a sequence that come as a tree
+
+struct CachedArgs {
+    // queries: the new tokens
+    const void* q;                  // [T, H, dqk]
+    int64_t q_stride;
+    const int64_t* ts;              // [T] or null
+    const int32_t* parents;         // [T] or null (each sequence a chain)
+    void* out;                      // [T, H, dv]
+    int64_t out_stride;
+    // the cache
+    const void* k;
+    const void* v;
+    int64_t k_page, k_tok, v_page, v_tok;       // elements
+    const int64_t* tsc;             // null without the time term
+    int64_t tsc_page;
+    int num_pages, shift;           // page_size = 1 << shift
+    const int32_t* table;           // [B, max_pages]
+    int64_t table_stride;
+    int max_pages;
+    // the batch
+    const int32_t* ctx;             // [B]
+    const int64_t* off;             // [B + 1]
+    int B;
+    int64_t T;
+    int max_new, max_seqlen;
+    int H, dqk, dv;
+    const float* pos;
+    int P;
+    const float* tb;
+    int NB;
+    float inv_n;
+    float* parts;                   // workspace: two parts a block
+};
+
+struct CachedSeq {
+    int64_t off;
+    int ctx, n;                     // n == 0: nothing to do
+};
+
+// Sequence b's numbers. A sequence that cannot be (negative lengths, offsets
+// outside [0, T], more new tokens than max_new or a tree's limit, longer than
+// max_seqlen or than a table row) is left out, `ok` false.
+__device__ __forceinline__ CachedSeq cached_seq(const CachedArgs& a, int b, bool& ok) {
+    const int64_t o = a.off[b], e = a.off[b + 1];
+    const int64_t c = a.ctx[b], n = e - o;
+    const int64_t room = static_cast<int64_t>(a.max_pages) << a.shift;
+    ok = c >= 0 && o >= 0 && n >= 0 && e <= a.T && n <= a.max_new && c + n <= a.max_seqlen &&
+         c + n <= room;
+    CachedSeq s;
+    s.off = o;
+    s.ctx = ok ? static_cast<int>(c) : 0;
+    s.n = ok ? static_cast<int>(n) : 0;
+    return s;
+}
+
+// Position on the line.
+struct LineAt {
+    int b, qt, h, j;                // j: key tile within the item
+    CachedSeq s;
+};
+
+template <int KT, int NQ>
+struct Line {
+    static __device__ __forceinline__ int tiles(const CachedSeq& s, int qt) {
+        return (s.ctx + min(s.n, (qt + 1) * NQ) + KT - 1) / KT;
+    }
+    // key tiles of one head of sequence s
+    static __device__ __forceinline__ int64_t per_head(const CachedSeq& s) {
+        int64_t w = 0;
+        for (int qt = 0; qt * NQ < s.n; ++qt) w += tiles(s, qt);
+        return w;
+    }
+    static __device__ __forceinline__ int64_t cut(int64_t total, int c, int blocks) {
+        return total * c / blocks;
+    }
+
+    // Block-wide: finds the line's length and the position of cut c. THREADS
+    // threads; `scratch` holds THREADS / 32 + 8 int64. Returns the length.
+    template <int THREADS>
+    static __device__ int64_t locate(const CachedArgs& a, int c, int blocks, int64_t* scratch,
+                                     LineAt& at, bool report) {
+        const int tid = threadIdx.x;
+        const int chunk = (a.B + THREADS - 1) / THREADS;
+        const int b0 = min(tid * chunk, a.B), b1 = min(b0 + chunk, a.B);
+        int64_t mine = 0;
+        bool all_ok = true;
+        for (int b = b0; b < b1; ++b) {
+            bool ok;
+            const CachedSeq s = cached_seq(a, b, ok);
+            all_ok = all_ok && ok && (b > 0 || s.off == 0) && (b + 1 < a.B || a.off[a.B] == a.T);
+            mine += per_head(s) * a.H;
+        }
+        if (report && !all_ok) raise_error(kErrBadInput);
+        int64_t scan = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, scan, o);
+            if ((tid & 31) >= o) scan += v;
+        }
+        if ((tid & 31) == 31) scratch[tid >> 5] = scan;
+        __syncthreads();
+        int64_t total = 0;
+#pragma unroll
+        for (int w = 0; w < THREADS / 32; ++w) {
+            if (w < (tid >> 5)) scan += scratch[w];
+            total += scratch[w];
+        }
+        const int64_t x = cut(total, c, blocks);
+        int64_t lo = scan - mine;
+        if (x >= lo && x < scan) {          // exactly one thread, when x < total
+            int b = b0;
+            CachedSeq s;
+            int64_t w;
+            while (true) {
+                bool ok;
+                s = cached_seq(a, b, ok);
+                w = per_head(s) * a.H;
+                if (x < lo + w) break;
+                lo += w;
+                ++b;
+            }
+            int64_t r = x - lo;
+            int qt = 0;
+            while (r >= static_cast<int64_t>(tiles(s, qt)) * a.H) {
+                r -= static_cast<int64_t>(tiles(s, qt)) * a.H;
+                ++qt;
+            }
+            const int nt = tiles(s, qt);
+            int64_t* f = scratch + THREADS / 32;
+            f[0] = b;
+            f[1] = qt;
+            f[2] = r / nt;
+            f[3] = r % nt;
+            f[4] = s.off;
+            f[5] = s.ctx;
+            f[6] = s.n;
+        }
+        __syncthreads();
+        if (x < total) {
+            const int64_t* f = scratch + THREADS / 32;
+            at.b = static_cast<int>(f[0]);
+            at.qt = static_cast<int>(f[1]);
+            at.h = static_cast<int>(f[2]);
+            at.j = static_cast<int>(f[3]);
+            at.s.off = f[4];
+            at.s.ctx = static_cast<int>(f[5]);
+            at.s.n = static_cast<int>(f[6]);
+        }
+        return total;
+    }
+
+    // The item after at's.
+    static __device__ __forceinline__ void next_item(const CachedArgs& a, LineAt& at) {
+        at.j = 0;
+        if (++at.h < a.H) return;
+        at.h = 0;
+        if (++at.qt * NQ < at.s.n) return;
+        at.qt = 0;
+        do {
+            if (++at.b >= a.B) return;
+            bool ok;
+            at.s = cached_seq(a, at.b, ok);
+        } while (at.s.n == 0);
+    }
+};
+
+// Parts: block c's first item at 2c, its last (when that is another) at 2c + 1,
+// NQ * DV floats each. The join: block c looks at cut c; where that is the
+// first cut inside an item (strictly behind its first tile), it adds the parts
+// of every block that shares the item and writes the item's rows.
+template <int KT, int NQ, typename TOut, int THREADS>
+__global__ void __launch_bounds__(THREADS) attn_cached_join_kernel(const CachedArgs a, int blocks) {
+    __shared__ int64_t scratch[THREADS / 32 + 8];
+    using L = Line<KT, NQ>;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int c = blockIdx.x + 1;           // cuts 1 .. blocks - 1
+    LineAt at;
+    const int64_t total = L::template locate<THREADS>(a, c, blocks, scratch, at, false);
+    const int64_t x = L::cut(total, c, blocks);
+    if (x >= total || at.j == 0) return;
+    const int64_t start = x - at.j, end = start + L::tiles(at.s, at.qt);
+    if (L::cut(total, c - 1, blocks) > start) return;       // an earlier cut lies inside too
+    // Blocks that share the item: c - 1, whose part is its last item's (its
+    // only one's when it begins with this item), then c, c + 1, ... while
+    // their parts begin inside.
+    const int part_len = NQ * a.dv;
+    const int rows = min(NQ, at.s.n - at.qt * NQ);
+    const int first = 2 * (c - 1) + (L::cut(total, c - 1, blocks) == start ? 0 : 1);
+    int last = c;
+    while (last + 1 < blocks && L::cut(total, last + 1, blocks) < end) ++last;
+    for (int i = threadIdx.x; i < rows * a.dv; i += THREADS) {
+        const int r = i / a.dv, col = i - r * a.dv;
+        float v = a.parts[static_cast<int64_t>(first) * part_len + i];
+        for (int p = c; p <= last; ++p)
+            if (L::cut(total, p, blocks) < L::cut(total, p + 1, blocks))   // empty parts have none
+                v += a.parts[static_cast<int64_t>(2 * p) * part_len + i];
+        TOut* dst = static_cast<TOut*>(a.out) + (at.s.off + at.qt * NQ + r) * a.out_stride +
+                    static_cast<int64_t>(at.h) * a.dv + col;
+        *dst = static_cast<TOut>(v * a.inv_n);
+    }
+}
+
+// ------------------------------------------------------------------ the tree
+
+// Who sees whom among a sequence's new tokens, for one tile of NQ queries
+// (64-bit word w of key m: queries 64w .. 64w + 63 of the tile that see m) and
+// the depth of every new token.
+struct alignas(16) TreeSmem {
+    uint32_t seen[kMaxTree / 32][kMaxTree];     // [query / 32][key]: bit of the query
+    int16_t depth[kMaxTree];
+    int16_t parent[kMaxTree];
+};
+
+// Built by `nt` threads (index t), which `sync` holds together; a parent that
+// is not before its token is an error and counts as -1.
+template <typename Sync>
+__device__ __forceinline__ void build_tree(const CachedArgs& a, const CachedSeq& s, TreeSmem& tree,
+                                           int t, int nt, Sync sync) {
+    sync();                                     // the previous tree is no longer read
+    const int words = (s.n + 31) / 32;
+    for (int m = t; m < s.n; m += nt) {
+        const int p = a.parents[s.off + m];
+        const bool ok = p >= -1 && p < m;
+        if (!ok) raise_error(kErrBadInput);
+        tree.parent[m] = static_cast<int16_t>(ok ? p : -1);
+        for (int w = 0; w < words; ++w) tree.seen[w][m] = 0u;
+    }
+    sync();
+    for (int m = t; m < s.n; m += nt) {
+        int d = -1;
+        for (int p = m; p >= 0; p = tree.parent[p]) {   // parents are smaller: ends
+            atomicOr(&tree.seen[m >> 5][p], 1u << (m & 31));
+            ++d;
+        }
+        tree.depth[m] = static_cast<int16_t>(d);
+    }
+    sync();
+}
+
+}  // namespace hstu

@@ -1,0 +1,227 @@
+// attn_cached_simt.cuh -- attention of new tokens over a paged cache on CUDA
+// cores, fp32 arithmetic (attn_cached.cuh has the formula and the work line).
+//
+// A block of 128 threads takes key tiles of 64 keys for tiles of 8 queries.
+// Scores: the tile's keys are copied to shared memory (rows padded by four
+// floats, so the 16-byte reads of eight lanes fall into different banks);
+// thread t has key t % 64 and four of the eight queries. Values: thread t has
+// column t % DMAX of the output and every (128 / DMAX)-th key, and reads V
+// straight from the cache, coalesced over the columns.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "attn_cached.cuh"
+
+namespace hstu {
+
+constexpr int kSimtKeys = 64;
+constexpr int kSimtRows = 8;
+constexpr int kSimtThreads = 128;
+constexpr int kSimtBlocks = 4 * 148;
+
+__device__ __forceinline__ float cached_load(const float* p) { return *p; }
+__device__ __forceinline__ float cached_load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+
+template <int DMAX>
+struct CachedSimtSmem {
+    alignas(16) float q[kSimtRows][DMAX];
+    alignas(16) float k[kSimtKeys][DMAX + 4];
+    alignas(16) float p[kSimtKeys][kSimtRows];
+    float red[kSimtRows][DMAX];
+    int64_t tk[kSimtKeys];
+    int64_t tq[kSimtRows];
+    int64_t scratch[kSimtThreads / 32 + 8];
+    int page[kSimtKeys];            // the key's page (its number in the cache), -1 none
+    int pk[kSimtKeys];
+    uint8_t vis[2][kSimtKeys];      // bit i of half h: query 4h + i sees the key
+    float tb[64];
+    TreeSmem tree;
+};
+
+// VEC: rows are 16-byte aligned and dqk a multiple of four (fp32)
+template <typename T, int DMAX, bool VEC>
+__global__ void __launch_bounds__(kSimtThreads) attn_cached_simt_kernel(const CachedArgs a) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    using S = CachedSimtSmem<DMAX>;
+    S& sm = *reinterpret_cast<S*>(smem_raw);
+    using L = Line<kSimtKeys, kSimtRows>;
+    constexpr int kGroups = kSimtThreads / DMAX;        // key groups of the value pass
+    const int tid = threadIdx.x;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    LineAt at;
+    const int64_t total = L::template locate<kSimtThreads>(a, blockIdx.x, gridDim.x, sm.scratch, at,
+                                                           blockIdx.x == 0);
+    const int64_t begin = L::cut(total, blockIdx.x, gridDim.x);
+    int64_t left = L::cut(total, blockIdx.x + 1, gridDim.x) - begin;
+    if (left <= 0) return;
+    const T* qp = static_cast<const T*>(a.q);
+    const T* kp = static_cast<const T*>(a.k);
+    const T* vp = static_cast<const T*>(a.v);
+    const int page_mask = (1 << a.shift) - 1;
+    const bool use_pos = a.pos != nullptr, use_time = a.tsc != nullptr;
+    int tree_of = -1, head_of = -1;
+    bool first_item = true;
+    while (left > 0) {
+        const int nt = L::tiles(at.s, at.qt);
+        const int take = static_cast<int>(min(left, static_cast<int64_t>(nt - at.j)));
+        const int q0 = at.qt * kSimtRows;
+        const int rows = min(kSimtRows, at.s.n - q0);
+        const int len = at.s.ctx + min(at.s.n, q0 + kSimtRows);
+        if (a.parents != nullptr && tree_of != at.b) {
+            build_tree(a, at.s, sm.tree, tid, kSimtThreads, [] { __syncthreads(); });
+            tree_of = at.b;
+        }
+        __syncthreads();
+        for (int i = tid; i < kSimtRows * DMAX; i += kSimtThreads) {
+            const int r = i / DMAX, c = i % DMAX;
+            float f = 0.f;
+            if (r < rows && c < a.dqk)
+                f = cached_load(qp + (at.s.off + q0 + r) * a.q_stride +
+                                static_cast<int64_t>(at.h) * a.dqk + c);
+            sm.q[r][c] = f;
+        }
+        if (tid < rows && use_time) sm.tq[tid] = a.ts[at.s.off + q0 + tid];
+        if (use_time && head_of != at.h) {
+            if (tid < 64) sm.tb[tid] = a.tb[static_cast<int64_t>(at.h) * a.NB + min(tid, a.NB - 1)];
+            head_of = at.h;
+        }
+        float acc[kSimtRows] = {};
+        const int col = tid % DMAX, grp = tid / DMAX;
+        for (int j = at.j; j < at.j + take; ++j) {
+            const int k0 = j * kSimtKeys, nk = min(kSimtKeys, len - k0);
+            // the tile's keys: page, position, timestamp
+            __syncthreads();
+            if (tid < kSimtKeys) {
+                int page = -1, pk = 0;
+                if (tid < nk) {
+                    const int key = k0 + tid;
+                    page = a.table[static_cast<int64_t>(at.b) * a.table_stride + (key >> a.shift)];
+                    if (page < 0 || page >= a.num_pages) {
+                        raise_error(kErrBadInput);
+                        page = -1;
+                    }
+                    pk = key;
+                    if (a.parents != nullptr && key >= at.s.ctx)
+                        pk = at.s.ctx + sm.tree.depth[key - at.s.ctx];
+                    if (use_time && page >= 0)
+                        sm.tk[tid] = a.tsc[page * a.tsc_page + (key & page_mask)];
+                }
+                sm.page[tid] = page;
+                sm.pk[tid] = pk;
+            }
+            __syncthreads();
+            if (VEC) {
+                const int nv = a.dqk / 4;
+                for (int i = tid; i < kSimtKeys * (DMAX / 4); i += kSimtThreads) {
+                    const int r = i / (DMAX / 4), c = i % (DMAX / 4);
+                    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (sm.page[r] >= 0 && c < nv)
+                        f = *reinterpret_cast<const float4*>(
+                            kp + sm.page[r] * a.k_page + ((k0 + r) & page_mask) * a.k_tok +
+                            static_cast<int64_t>(at.h) * a.dqk + 4 * c);
+                    *reinterpret_cast<float4*>(&sm.k[r][4 * c]) = f;
+                }
+            } else {
+                for (int i = tid; i < kSimtKeys * DMAX; i += kSimtThreads) {
+                    const int r = i / DMAX, c = i % DMAX;
+                    float f = 0.f;
+                    if (sm.page[r] >= 0 && c < a.dqk)
+                        f = cached_load(kp + sm.page[r] * a.k_page + ((k0 + r) & page_mask) * a.k_tok +
+                                        static_cast<int64_t>(at.h) * a.dqk + c);
+                    sm.k[r][c] = f;
+                }
+            }
+            __syncthreads();
+            // scores of key tid % 64, queries 4 (tid / 64) ..
+            {
+                const int r = tid % kSimtKeys, i0 = (tid / kSimtKeys) * 4;
+                float s[4] = {};
+                for (int c = 0; c < a.dqk; c += 4) {
+                    const float4 kv = *reinterpret_cast<const float4*>(&sm.k[r][c]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 qv = *reinterpret_cast<const float4*>(&sm.q[i0 + i][c]);
+                        s[i] = fmaf(kv.x, qv.x, s[i]);
+                        s[i] = fmaf(kv.y, qv.y, s[i]);
+                        s[i] = fmaf(kv.z, qv.z, s[i]);
+                        s[i] = fmaf(kv.w, qv.w, s[i]);
+                    }
+                }
+                const int m = k0 + r - at.s.ctx;        // new token's index, < 0: cached
+                uint32_t vis = 0u;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int qi = q0 + i0 + i;
+                    bool see = sm.page[r] >= 0 && i0 + i < rows;
+                    if (m >= 0)
+                        see = see && (a.parents != nullptr
+                                          ? ((sm.tree.seen[qi >> 5][m] >> (qi & 31)) & 1u) != 0u
+                                          : m <= qi);
+                    float p = 0.f;
+                    if (see) {
+                        const int pq = at.s.ctx + (a.parents != nullptr ? sm.tree.depth[qi] : qi);
+                        float x = s[i];
+                        if (use_pos)
+                            x += a.pos[static_cast<int64_t>(at.h) * a.P + min(pq - sm.pk[r], a.P - 1)];
+                        if (use_time) x += sm.tb[time_bucket64(sm.tq[i0 + i] - sm.tk[r], 63)];
+                        p = x / (1.f + expf(-x));
+                        vis |= 1u << i;
+                    }
+                    sm.p[r][i0 + i] = p;
+                }
+                sm.vis[i0 / 4][r] = static_cast<uint8_t>(vis);
+            }
+            __syncthreads();
+            if (col < a.dv) {
+                for (int r = grp; r < nk; r += kGroups) {
+                    const int page = sm.page[r];
+                    if (page < 0) continue;
+                    const float v = cached_load(vp + page * a.v_page + ((k0 + r) & page_mask) * a.v_tok +
+                                                static_cast<int64_t>(at.h) * a.dv + col);
+                    // a key that a query does not see adds nothing, whatever its value
+                    // is (not 0 * v, which is NaN for a v that is not finite)
+                    const uint32_t vis = sm.vis[0][r] | (static_cast<uint32_t>(sm.vis[1][r]) << 4);
+#pragma unroll
+                    for (int i = 0; i < kSimtRows; ++i)
+                        if ((vis >> i) & 1u) acc[i] = fmaf(sm.p[r][i], v, acc[i]);
+                }
+            }
+        }
+        // sum over the key groups, then the rows (or this block's part of them)
+        if (kGroups > 1) {
+            for (int g = 1; g < kGroups; ++g) {
+                __syncthreads();
+                if (grp == g) {
+#pragma unroll
+                    for (int i = 0; i < kSimtRows; ++i) sm.red[i][col] = acc[i];
+                }
+                __syncthreads();
+                if (grp == 0) {
+#pragma unroll
+                    for (int i = 0; i < kSimtRows; ++i) acc[i] += sm.red[i][col];
+                }
+            }
+        }
+        if (grp == 0 && col < a.dv) {
+            const bool whole = take == nt;
+            float* part = a.parts + (2 * static_cast<int64_t>(blockIdx.x) + (first_item ? 0 : 1)) *
+                                        kSimtRows * a.dv;
+#pragma unroll
+            for (int i = 0; i < kSimtRows; ++i) {
+                if (i >= rows) break;
+                if (whole)
+                    static_cast<T*>(a.out)[(at.s.off + q0 + i) * a.out_stride +
+                                           static_cast<int64_t>(at.h) * a.dv + col] =
+                        static_cast<T>(acc[i] * a.inv_n);
+                else
+                    part[i * a.dv + col] = acc[i];
+            }
+        }
+        left -= take;
+        first_item = false;
+        if (left > 0) L::next_item(a, at);
+    }
+}
+
+}  // namespace hstu

@@ -1,0 +1,299 @@
+// cache_api.cuh -- host side of the serving entry points: the paged cache
+// (plan, append, attention over it) and projections with 4-bit weights.
+// Included once, by hstu_api.cu, after its helpers.
+#pragma once
+
+#include "attn_cached.cuh"
+#include "attn_cached_simt.cuh"
+#include "cache_plan.cuh"
+#include "linear_w4.cuh"
+
+namespace {
+
+// log2 of a supported page size, -1 otherwise
+int page_shift(int32_t page_size) {
+    if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1))) return -1;
+    int s = 0;
+    while ((1 << s) < page_size) ++s;
+    return s;
+}
+
+bool cache_size_ok(int32_t num_pages, int32_t page_size) {
+    return num_pages >= 1 && page_size >= 1 &&
+           static_cast<int64_t>(num_pages) * page_size <= 0x7fffffff;
+}
+
+hstu_status_t validate_cached(hstu_dtype_t dtype, const CachedArgs& c, int32_t page_size,
+                              const void* ws, size_t ws_bytes, size_t need) {
+    if (c.B < 0 || c.T < 0 || c.T > 0x7fffffff || c.H < 1 || c.dqk < 1 || c.dv < 1 ||
+        c.max_new < 1 || c.max_seqlen < 1 || c.max_seqlen > kMaxSeqlen || c.max_pages < 1)
+        return HSTU_ERR_INVALID_ARG;
+    if (dtype != HSTU_DTYPE_F32 && dtype != HSTU_DTYPE_BF16) return HSTU_ERR_INVALID_ARG;
+    if (c.shift < 0) return HSTU_ERR_UNSUPPORTED;
+    if (!cache_size_ok(c.num_pages, page_size)) return HSTU_ERR_INVALID_ARG;
+    if (c.pos && c.P < 1) return HSTU_ERR_INVALID_ARG;
+    if (c.tb && (c.NB < 1 || c.NB > kMaxTimeBuckets)) return HSTU_ERR_INVALID_ARG;
+    if (c.parents && c.max_new > kMaxTree) return HSTU_ERR_UNSUPPORTED;
+    if (c.H > 65535) return HSTU_ERR_UNSUPPORTED;
+    if (dtype == HSTU_DTYPE_BF16) {
+        if (c.dqk != c.dv || (c.dqk != 32 && c.dqk != 64 && c.dqk != 128))
+            return HSTU_ERR_UNSUPPORTED;
+    } else if (c.dqk > 128 || c.dv > 128) {
+        return HSTU_ERR_UNSUPPORTED;
+    }
+    if (c.B == 0 || c.T == 0) return HSTU_OK;
+    const int64_t rq = static_cast<int64_t>(c.H) * c.dqk, rv = static_cast<int64_t>(c.H) * c.dv;
+    if (!c.q || !c.k || !c.v || !c.out || !c.table || !c.ctx || !c.off) return HSTU_ERR_INVALID_ARG;
+    if (c.q_stride < rq || c.out_stride < rv || c.k_tok < rq || c.v_tok < rv ||
+        c.table_stride < c.max_pages)
+        return HSTU_ERR_INVALID_ARG;
+    if (c.k_page < (page_size - 1) * c.k_tok + rq || c.v_page < (page_size - 1) * c.v_tok + rv)
+        return HSTU_ERR_INVALID_ARG;
+    if (c.tsc && c.tsc_page < page_size) return HSTU_ERR_INVALID_ARG;
+    if (dtype == HSTU_DTYPE_BF16) {
+        if (!aligned16(c.q) || !aligned16(c.k) || !aligned16(c.v) || !aligned16(c.out))
+            return HSTU_ERR_INVALID_ARG;
+        if (c.q_stride % 8 || c.out_stride % 8 || c.k_tok % 8 || c.v_tok % 8 || c.k_page % 8 ||
+            c.v_page % 8)
+            return HSTU_ERR_INVALID_ARG;
+    }
+    if (!ws || !aligned16(ws) || ws_bytes < need) return HSTU_ERR_INVALID_ARG;
+    return HSTU_OK;
+}
+
+// The join of parts, as a programmatic dependent of the attention launch.
+template <int KT, int NQ, typename TOut>
+hstu_status_t launch_join(const CachedArgs& a, int blocks, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks - 1));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_cached_join_kernel<KT, NQ, TOut, 256>, a,
+                                             blocks);
+    return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+}
+
+template <typename T, int DMAX, bool VEC>
+hstu_status_t launch_cached_simt(const CachedArgs& a, cudaStream_t stream) {
+    static int done[kMaxDevices] = {0};
+    constexpr int smem = static_cast<int>(sizeof(CachedSimtSmem<DMAX>));
+    if (!ensure_smem(attn_cached_simt_kernel<T, DMAX, VEC>, smem, done)) return HSTU_ERR_CUDA;
+    attn_cached_simt_kernel<T, DMAX, VEC><<<kSimtBlocks, kSimtThreads, smem, stream>>>(a);
+    const hstu_status_t st = launch_status();
+    return st == HSTU_OK ? launch_join<kSimtKeys, kSimtRows, T>(a, kSimtBlocks, stream) : st;
+}
+
+template <typename T, bool VEC>
+hstu_status_t run_cached_simt(const CachedArgs& a, cudaStream_t stream) {
+    const int d = a.dqk > a.dv ? a.dqk : a.dv;
+    if (d <= 32) return launch_cached_simt<T, 32, VEC>(a, stream);
+    if (d <= 64) return launch_cached_simt<T, 64, VEC>(a, stream);
+    return launch_cached_simt<T, 128, VEC>(a, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+hstu_status_t hstu_cache_plan(const int32_t* ctx_lens, const int64_t* new_offsets, int32_t B,
+                              int64_t total_new, int32_t page_size, const int32_t* free_pages,
+                              int32_t num_free, const int32_t* free_start, int32_t* block_table,
+                              int64_t table_stride, int32_t max_pages, int64_t* slots,
+                              int32_t* free_end, void* stream) {
+    if (B < 1 || total_new < 0 || total_new > 0x7fffffff || num_free < 0 || max_pages < 1 ||
+        table_stride < max_pages)
+        return HSTU_ERR_INVALID_ARG;
+    const int shift = page_shift(page_size);
+    if (shift < 0) return HSTU_ERR_UNSUPPORTED;
+    if (!cache_size_ok(max_pages, page_size)) return HSTU_ERR_UNSUPPORTED;
+    if (!ctx_lens || !new_offsets || !free_start || !block_table || !free_end || free_end == free_start ||
+        (num_free > 0 && !free_pages) || (total_new > 0 && !slots))
+        return HSTU_ERR_INVALID_ARG;
+    CachePlanArgs a{ctx_lens, new_offsets, B, total_new, shift, free_pages, num_free, free_start,
+                    block_table, table_stride, max_pages, slots, free_end, 1};
+    // up to two blocks an SM over the sequences, then over each block's tokens
+    int s = (B + 295) / 296;
+    a.seqs_per_block = s > kPlanSeqs ? kPlanSeqs : s;
+    const unsigned gx = static_cast<unsigned>((B + a.seqs_per_block - 1) / a.seqs_per_block);
+    const int64_t per = (total_new / gx + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
+    const int64_t most = gx >= 296 ? 1 : 296 / gx;
+    const unsigned gy = static_cast<unsigned>(per < 1 ? 1 : per < most ? per : most);
+    cache_plan_kernel<<<dim3(gx, gy), kPlanThreads, 0, as_stream(stream)>>>(a);
+    return launch_status();
+}
+
+hstu_status_t hstu_cache_append(hstu_dtype_t dtype, const void* k, int64_t k_stride, const void* v,
+                                int64_t v_stride, const int64_t* timestamps, const int64_t* slots,
+                                int64_t total_new, int32_t H, int32_t d_qk, int32_t d_v,
+                                void* k_cache, int64_t k_page_stride, int64_t k_tok_stride,
+                                void* v_cache, int64_t v_page_stride, int64_t v_tok_stride,
+                                int64_t* ts_cache, int64_t ts_page_stride, int32_t num_pages,
+                                int32_t page_size, void* stream) {
+    if (dtype != HSTU_DTYPE_F32 && dtype != HSTU_DTYPE_BF16) return HSTU_ERR_INVALID_ARG;
+    if (total_new < 0 || H < 1 || d_qk < 1 || d_v < 1) return HSTU_ERR_INVALID_ARG;
+    const int shift = page_shift(page_size);
+    if (shift < 0) return HSTU_ERR_UNSUPPORTED;
+    if (!cache_size_ok(num_pages, page_size)) return HSTU_ERR_INVALID_ARG;
+    const int64_t rk = static_cast<int64_t>(H) * d_qk, rv = static_cast<int64_t>(H) * d_v;
+    if (rk > (1 << 28) || rv > (1 << 28)) return HSTU_ERR_UNSUPPORTED;
+    if (k_tok_stride < rk || v_tok_stride < rv ||
+        k_page_stride < (page_size - 1) * k_tok_stride + rk ||
+        v_page_stride < (page_size - 1) * v_tok_stride + rv)
+        return HSTU_ERR_INVALID_ARG;
+    if ((timestamps == nullptr) != (ts_cache == nullptr)) return HSTU_ERR_INVALID_ARG;
+    if (ts_cache && ts_page_stride < page_size) return HSTU_ERR_INVALID_ARG;
+    if (total_new == 0) return HSTU_OK;
+    if (!k || !v || !slots || !k_cache || !v_cache) return HSTU_ERR_INVALID_ARG;
+    if (total_new > 1 && (k_stride < rk || v_stride < rv)) return HSTU_ERR_INVALID_ARG;
+    const int e = dtype == HSTU_DTYPE_BF16 ? 2 : 4;
+    CacheAppendArgs a{static_cast<const uint8_t*>(k), static_cast<const uint8_t*>(v), k_stride * e,
+                      v_stride * e, static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache),
+                      k_page_stride * e, k_tok_stride * e, v_page_stride * e, v_tok_stride * e,
+                      static_cast<int>(rk * e), static_cast<int>(rv * e), timestamps, ts_cache,
+                      ts_page_stride, slots, total_new,
+                      static_cast<int64_t>(num_pages) * page_size, shift};
+    const uint64_t mix = reinterpret_cast<uint64_t>(k) | reinterpret_cast<uint64_t>(v) |
+                         reinterpret_cast<uint64_t>(k_cache) | reinterpret_cast<uint64_t>(v_cache) |
+                         a.k_stride | a.v_stride | a.kc_page | a.kc_tok | a.vc_page | a.vc_tok |
+                         a.k_bytes | a.v_bytes;
+    if (mix % e) return HSTU_ERR_INVALID_ARG;
+    const int64_t blocks = (total_new + kAppendWarps - 1) / kAppendWarps;
+    const unsigned grid = static_cast<unsigned>(blocks < 8 * 148 ? blocks : 8 * 148);
+    cudaStream_t s = as_stream(stream);
+    if (mix % 16 == 0) cache_append_kernel<uint4><<<grid, kAppendWarps * 32, 0, s>>>(a);
+    else if (mix % 4 == 0) cache_append_kernel<uint32_t><<<grid, kAppendWarps * 32, 0, s>>>(a);
+    else cache_append_kernel<uint16_t><<<grid, kAppendWarps * 32, 0, s>>>(a);
+    return launch_status();
+}
+
+size_t hstu_attn_cached_workspace_bytes(hstu_dtype_t dtype, int32_t max_new, int32_t d_v) {
+    if ((dtype != HSTU_DTYPE_F32 && dtype != HSTU_DTYPE_BF16) || max_new < 1 || d_v < 1 ||
+        d_v > 128)
+        return 0;
+    return static_cast<size_t>(2) * kSimtBlocks * kSimtRows * d_v * 4;
+}
+
+hstu_status_t hstu_attn_cached_fwd(hstu_dtype_t dtype, const void* q, int64_t q_tok_stride,
+                                   const void* k_cache, int64_t k_page_stride,
+                                   int64_t k_tok_stride, const void* v_cache,
+                                   int64_t v_page_stride, int64_t v_tok_stride,
+                                   const int64_t* ts_cache, int64_t ts_page_stride,
+                                   int32_t num_pages, int32_t page_size,
+                                   const int32_t* block_table, int64_t table_stride,
+                                   int32_t max_pages, const int32_t* ctx_lens,
+                                   const int64_t* new_offsets, int32_t B, int64_t total_new,
+                                   int32_t max_new, int32_t H, int32_t d_qk, int32_t d_v,
+                                   const int64_t* timestamps, const int32_t* parents,
+                                   const float* pos_bias, int32_t num_pos, const float* time_bias,
+                                   int32_t num_time_buckets, int32_t max_seqlen, void* out,
+                                   int64_t out_tok_stride, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+    const bool use_time = ts_cache && timestamps && time_bias;
+    CachedArgs a{};
+    a.q = q;
+    a.q_stride = q_tok_stride;
+    a.ts = use_time ? timestamps : nullptr;
+    a.parents = parents;
+    a.out = out;
+    a.out_stride = out_tok_stride;
+    a.k = k_cache;
+    a.v = v_cache;
+    a.k_page = k_page_stride;
+    a.k_tok = k_tok_stride;
+    a.v_page = v_page_stride;
+    a.v_tok = v_tok_stride;
+    a.tsc = use_time ? ts_cache : nullptr;
+    a.tsc_page = ts_page_stride;
+    a.num_pages = num_pages;
+    a.shift = page_shift(page_size);
+    a.table = block_table;
+    a.table_stride = table_stride;
+    a.max_pages = max_pages;
+    a.ctx = ctx_lens;
+    a.off = new_offsets;
+    a.B = B;
+    a.T = total_new;
+    a.max_new = max_new;
+    a.max_seqlen = max_seqlen;
+    a.H = H;
+    a.dqk = d_qk;
+    a.dv = d_v;
+    a.pos = pos_bias;
+    a.P = num_pos;
+    a.tb = use_time ? time_bias : nullptr;
+    a.NB = num_time_buckets;
+    a.inv_n = 1.0f / static_cast<float>(max_seqlen);
+    a.parts = static_cast<float*>(workspace);
+    const hstu_status_t st =
+        validate_cached(dtype, a, page_size, workspace, workspace_bytes,
+                        hstu_attn_cached_workspace_bytes(dtype, max_new, d_v));
+    if (st != HSTU_OK || B == 0 || total_new == 0) return st;
+    if (dtype == HSTU_DTYPE_BF16) return run_cached_simt<__nv_bfloat16, false>(a, as_stream(stream));
+    const bool vec = aligned16(k_cache) && k_page_stride % 4 == 0 && k_tok_stride % 4 == 0 &&
+                     d_qk % 4 == 0;
+    return vec ? run_cached_simt<float, true>(a, as_stream(stream))
+               : run_cached_simt<float, false>(a, as_stream(stream));
+}
+
+hstu_status_t hstu_quant_groups_w4(const void* W, int64_t ldw, int64_t N, int32_t K, int32_t group,
+                                   void* codes, int64_t ldc, void* scales, int64_t lds,
+                                   void* stream) {
+    if (N < 0 || K < 1) return HSTU_ERR_INVALID_ARG;
+    if ((group != 32 && group != 64 && group != 128) || K % group) return HSTU_ERR_UNSUPPORTED;
+    if (N == 0) return HSTU_OK;
+    if (!W || !codes || !scales || ldw < K || ldc < K / 2 || lds < K / group)
+        return HSTU_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(W) % 2 || reinterpret_cast<uintptr_t>(scales) % 2)
+        return HSTU_ERR_INVALID_ARG;
+    const QuantW4Args a{static_cast<const __nv_bfloat16*>(W), ldw, N, K,
+                        static_cast<uint8_t*>(codes), ldc, static_cast<__nv_bfloat16*>(scales),
+                        lds};
+    const int64_t warps = (N * (K / group) * (group / (group == 128 ? 4 : 2)) + 31) / 32;
+    const int64_t blocks = (warps + 7) / 8;
+    const unsigned grid = static_cast<unsigned>(blocks < 16 * 148 ? blocks : 16 * 148);
+    cudaStream_t s = as_stream(stream);
+    if (group == 32) quant_w4_kernel<32><<<grid, 256, 0, s>>>(a);
+    else if (group == 64) quant_w4_kernel<64><<<grid, 256, 0, s>>>(a);
+    else quant_w4_kernel<128><<<grid, 256, 0, s>>>(a);
+    return launch_status();
+}
+
+hstu_status_t hstu_linear_w4_fwd(const void* x, int64_t ldx, int64_t M, int32_t K, const void* codes,
+                                 int64_t ldc, const void* scales, int64_t lds, int32_t group,
+                                 int32_t N, const float* bias, hstu_epilogue_t epilogue,
+                                 const void* residual, int64_t ldr, void* y, int64_t ldy,
+                                 void* stream) {
+    if (M < 0 || K < 1 || N < 1) return HSTU_ERR_INVALID_ARG;
+    if (epilogue != HSTU_EPI_NONE && epilogue != HSTU_EPI_SILU && epilogue != HSTU_EPI_RESIDUAL)
+        return HSTU_ERR_INVALID_ARG;
+    if ((group != 32 && group != 64 && group != 128) || K % 128 || M > 65535 * 8)
+        return HSTU_ERR_UNSUPPORTED;
+    if (M == 0) return HSTU_OK;
+    if (!x || !codes || !scales || !y || (epilogue == HSTU_EPI_RESIDUAL && !residual))
+        return HSTU_ERR_INVALID_ARG;
+    if (ldx < K || ldc < K / 2 || lds < K / group || ldy < N ||
+        (epilogue == HSTU_EPI_RESIDUAL && ldr < N))
+        return HSTU_ERR_INVALID_ARG;
+    if (!aligned16(x) || ldx % 8 || !aligned16(codes) || ldc % 16) return HSTU_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(scales) % 2 || reinterpret_cast<uintptr_t>(y) % 2 ||
+        reinterpret_cast<uintptr_t>(residual) % 2 || reinterpret_cast<uintptr_t>(bias) % 4)
+        return HSTU_ERR_INVALID_ARG;
+    LinearW4Args a{static_cast<const __nv_bfloat16*>(x), ldx, static_cast<int>(M), K, N, group,
+                   static_cast<const uint8_t*>(codes), ldc,
+                   static_cast<const __nv_bfloat16*>(scales), lds, bias,
+                   static_cast<const __nv_bfloat16*>(residual), ldr,
+                   static_cast<__nv_bfloat16*>(y), ldy};
+    const dim3 grid(static_cast<unsigned>((N + 3) / 4), static_cast<unsigned>((M + 7) / 8));
+    cudaStream_t s = as_stream(stream);
+    if (epilogue == HSTU_EPI_SILU) linear_w4_kernel<1><<<grid, 128, 0, s>>>(a);
+    else if (epilogue == HSTU_EPI_RESIDUAL) linear_w4_kernel<2><<<grid, 128, 0, s>>>(a);
+    else linear_w4_kernel<0><<<grid, 128, 0, s>>>(a);
+    return launch_status();
+}
+
+}  // extern "C"

@@ -1055,3 +1055,5 @@ extern "C" hstu_status_t hstu_attn_fwd_noalloc(
                          scratch ? HSTU_NOALLOC_SCRATCH_BYTES : 0, stream);
 }
 
+
+#include "cache_api.cuh"
