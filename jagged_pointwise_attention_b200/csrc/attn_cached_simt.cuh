@@ -9,8 +9,6 @@
 // straight from the cache, coalesced over the columns.
 #pragma once
 
-#include <cuda_bf16.h>
-
 #include "attn_cached.cuh"
 
 namespace hstu {
@@ -19,9 +17,6 @@ constexpr int kSimtKeys = 64;
 constexpr int kSimtRows = 8;
 constexpr int kSimtThreads = 128;
 constexpr int kSimtBlocks = 4 * 148;
-
-__device__ __forceinline__ float cached_load(const float* p) { return *p; }
-__device__ __forceinline__ float cached_load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
 template <int DMAX>
 struct CachedSimtSmem {
@@ -39,8 +34,8 @@ struct CachedSimtSmem {
     TreeSmem tree;
 };
 
-// VEC: rows are 16-byte aligned and dqk a multiple of four (fp32)
-template <typename T, int DMAX, bool VEC>
+// VEC: rows are 16-byte aligned and dqk a multiple of four
+template <int DMAX, bool VEC>
 __global__ void __launch_bounds__(kSimtThreads) attn_cached_simt_kernel(const CachedArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     using S = CachedSimtSmem<DMAX>;
@@ -55,9 +50,9 @@ __global__ void __launch_bounds__(kSimtThreads) attn_cached_simt_kernel(const Ca
     const int64_t begin = L::cut(total, blockIdx.x, gridDim.x);
     int64_t left = L::cut(total, blockIdx.x + 1, gridDim.x) - begin;
     if (left <= 0) return;
-    const T* qp = static_cast<const T*>(a.q);
-    const T* kp = static_cast<const T*>(a.k);
-    const T* vp = static_cast<const T*>(a.v);
+    const float* qp = static_cast<const float*>(a.q);
+    const float* kp = static_cast<const float*>(a.k);
+    const float* vp = static_cast<const float*>(a.v);
     const int page_mask = (1 << a.shift) - 1;
     const bool use_pos = a.pos != nullptr, use_time = a.tsc != nullptr;
     int tree_of = -1, head_of = -1;
@@ -77,8 +72,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_cached_simt_kernel(const Ca
             const int r = i / DMAX, c = i % DMAX;
             float f = 0.f;
             if (r < rows && c < a.dqk)
-                f = cached_load(qp + (at.s.off + q0 + r) * a.q_stride +
-                                static_cast<int64_t>(at.h) * a.dqk + c);
+                f = qp[(at.s.off + q0 + r) * a.q_stride + static_cast<int64_t>(at.h) * a.dqk + c];
             sm.q[r][c] = f;
         }
         if (tid < rows && use_time) sm.tq[tid] = a.ts[at.s.off + q0 + tid];
@@ -127,8 +121,8 @@ __global__ void __launch_bounds__(kSimtThreads) attn_cached_simt_kernel(const Ca
                     const int r = i / DMAX, c = i % DMAX;
                     float f = 0.f;
                     if (sm.page[r] >= 0 && c < a.dqk)
-                        f = cached_load(kp + sm.page[r] * a.k_page + ((k0 + r) & page_mask) * a.k_tok +
-                                        static_cast<int64_t>(at.h) * a.dqk + c);
+                        f = kp[sm.page[r] * a.k_page + ((k0 + r) & page_mask) * a.k_tok +
+                               static_cast<int64_t>(at.h) * a.dqk + c];
                     sm.k[r][c] = f;
                 }
             }
@@ -177,8 +171,8 @@ __global__ void __launch_bounds__(kSimtThreads) attn_cached_simt_kernel(const Ca
                 for (int r = grp; r < nk; r += kGroups) {
                     const int page = sm.page[r];
                     if (page < 0) continue;
-                    const float v = cached_load(vp + page * a.v_page + ((k0 + r) & page_mask) * a.v_tok +
-                                                static_cast<int64_t>(at.h) * a.dv + col);
+                    const float v = vp[page * a.v_page + ((k0 + r) & page_mask) * a.v_tok +
+                                       static_cast<int64_t>(at.h) * a.dv + col];
                     // a key that a query does not see adds nothing, whatever its value
                     // is (not 0 * v, which is NaN for a v that is not finite)
                     const uint32_t vis = sm.vis[0][r] | (static_cast<uint32_t>(sm.vis[1][r]) << 4);
@@ -211,9 +205,9 @@ __global__ void __launch_bounds__(kSimtThreads) attn_cached_simt_kernel(const Ca
             for (int i = 0; i < kSimtRows; ++i) {
                 if (i >= rows) break;
                 if (whole)
-                    static_cast<T*>(a.out)[(at.s.off + q0 + i) * a.out_stride +
-                                           static_cast<int64_t>(at.h) * a.dv + col] =
-                        static_cast<T>(acc[i] * a.inv_n);
+                    static_cast<float*>(a.out)[(at.s.off + q0 + i) * a.out_stride +
+                                               static_cast<int64_t>(at.h) * a.dv + col] =
+                        acc[i] * a.inv_n;
                 else
                     part[i * a.dv + col] = acc[i];
             }

@@ -4,6 +4,7 @@
 #pragma once
 
 #include "attn_cached.cuh"
+#include "attn_cached_mma.cuh"
 #include "attn_cached_simt.cuh"
 #include "cache_plan.cuh"
 #include "linear_w4.cuh"
@@ -78,22 +79,82 @@ hstu_status_t launch_join(const CachedArgs& a, int blocks, cudaStream_t stream) 
     return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }
 
-template <typename T, int DMAX, bool VEC>
+template <int DMAX, bool VEC>
 hstu_status_t launch_cached_simt(const CachedArgs& a, cudaStream_t stream) {
     static int done[kMaxDevices] = {0};
     constexpr int smem = static_cast<int>(sizeof(CachedSimtSmem<DMAX>));
-    if (!ensure_smem(attn_cached_simt_kernel<T, DMAX, VEC>, smem, done)) return HSTU_ERR_CUDA;
-    attn_cached_simt_kernel<T, DMAX, VEC><<<kSimtBlocks, kSimtThreads, smem, stream>>>(a);
+    if (!ensure_smem(attn_cached_simt_kernel<DMAX, VEC>, smem, done)) return HSTU_ERR_CUDA;
+    attn_cached_simt_kernel<DMAX, VEC><<<kSimtBlocks, kSimtThreads, smem, stream>>>(a);
     const hstu_status_t st = launch_status();
-    return st == HSTU_OK ? launch_join<kSimtKeys, kSimtRows, T>(a, kSimtBlocks, stream) : st;
+    return st == HSTU_OK ? launch_join<kSimtKeys, kSimtRows, float>(a, kSimtBlocks, stream) : st;
 }
 
-template <typename T, bool VEC>
+template <bool VEC>
 hstu_status_t run_cached_simt(const CachedArgs& a, cudaStream_t stream) {
     const int d = a.dqk > a.dv ? a.dqk : a.dv;
-    if (d <= 32) return launch_cached_simt<T, 32, VEC>(a, stream);
-    if (d <= 64) return launch_cached_simt<T, 64, VEC>(a, stream);
-    return launch_cached_simt<T, 128, VEC>(a, stream);
+    if (d <= 32) return launch_cached_simt<32, VEC>(a, stream);
+    if (d <= 64) return launch_cached_simt<64, VEC>(a, stream);
+    return launch_cached_simt<128, VEC>(a, stream);
+}
+
+// bf16 [pages, page_size, H d] of a cache, boxes of 16 tokens x 64 (32) columns.
+bool make_tmap_cache(CUtensorMap* tm, const void* base, const CachedArgs& a, int64_t page,
+                     int64_t tok) {
+    auto fn = encode_fn();
+    if (fn == nullptr) return false;
+    const int d = a.dqk;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.H) * d, cuuint64_t{1} << a.shift,
+                          static_cast<cuuint64_t>(a.num_pages)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(tok) * 2, static_cast<cuuint64_t>(page) * 2};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(d >= 64 ? 64 : 32), kMmaKeys, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          d >= 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+constexpr int kMmaBlocks = 148;
+// Sequences up to this length are taken whole by a block each: at most eight
+// groups a warp, less than the search of the line and the join cost.
+constexpr int kWholeLen = 1024;
+
+template <int D, int NT>
+hstu_status_t launch_cached_mma(const CachedArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
+                                cudaStream_t stream) {
+    using S = CachedMmaSmem<D, NT>;
+    const int qtiles = (a.max_new + S::kNQ - 1) / S::kNQ;
+    const int64_t items = static_cast<int64_t>(a.B) * qtiles * a.H;
+    if (a.max_seqlen <= kWholeLen && items <= 0x7fffffff) {
+        static int done[kMaxDevices] = {0};
+        if (!ensure_smem(attn_cached_mma_kernel<D, NT, true>, S::kAlloc, done)) return HSTU_ERR_CUDA;
+        attn_cached_mma_kernel<D, NT, true>
+            <<<static_cast<unsigned>(items), kMmaThreads, S::kAlloc, stream>>>(tk, tv, a, qtiles);
+        return launch_status();
+    }
+    static int done[kMaxDevices] = {0};
+    if (!ensure_smem(attn_cached_mma_kernel<D, NT, false>, S::kAlloc, done)) return HSTU_ERR_CUDA;
+    attn_cached_mma_kernel<D, NT, false>
+        <<<kMmaBlocks, kMmaThreads, S::kAlloc, stream>>>(tk, tv, a, qtiles);
+    const hstu_status_t st = launch_status();
+    return st == HSTU_OK ? launch_join<kMmaKeys, S::kNQ, __nv_bfloat16>(a, kMmaBlocks, stream) : st;
+}
+
+// query tiles of 8 NT rows
+int cached_nt(int32_t max_new) { return max_new <= 8 ? 1 : max_new <= 16 ? 2 : 4; }
+
+template <int D>
+hstu_status_t run_cached_mma(const CachedArgs& a, cudaStream_t stream) {
+    CUtensorMap tk, tv;
+    if (!make_tmap_cache(&tk, a.k, a, a.k_page, a.k_tok) ||
+        !make_tmap_cache(&tv, a.v, a, a.v_page, a.v_tok))
+        return HSTU_ERR_CUDA;
+    switch (cached_nt(a.max_new)) {
+        case 1: return launch_cached_mma<D, 1>(a, tk, tv, stream);
+        case 2: return launch_cached_mma<D, 2>(a, tk, tv, stream);
+        default: return launch_cached_mma<D, 4>(a, tk, tv, stream);
+    }
 }
 
 }  // namespace
@@ -175,7 +236,9 @@ size_t hstu_attn_cached_workspace_bytes(hstu_dtype_t dtype, int32_t max_new, int
     if ((dtype != HSTU_DTYPE_F32 && dtype != HSTU_DTYPE_BF16) || max_new < 1 || d_v < 1 ||
         d_v > 128)
         return 0;
-    return static_cast<size_t>(2) * kSimtBlocks * kSimtRows * d_v * 4;
+    const size_t rows = dtype == HSTU_DTYPE_F32 ? static_cast<size_t>(kSimtBlocks) * kSimtRows
+                                                : static_cast<size_t>(kMmaBlocks) * 8 * cached_nt(max_new);
+    return 2 * rows * d_v * 4;
 }
 
 hstu_status_t hstu_attn_cached_fwd(hstu_dtype_t dtype, const void* q, int64_t q_tok_stride,
@@ -233,11 +296,15 @@ hstu_status_t hstu_attn_cached_fwd(hstu_dtype_t dtype, const void* q, int64_t q_
         validate_cached(dtype, a, page_size, workspace, workspace_bytes,
                         hstu_attn_cached_workspace_bytes(dtype, max_new, d_v));
     if (st != HSTU_OK || B == 0 || total_new == 0) return st;
-    if (dtype == HSTU_DTYPE_BF16) return run_cached_simt<__nv_bfloat16, false>(a, as_stream(stream));
+    if (dtype == HSTU_DTYPE_BF16) {
+        if (d_qk == 32) return run_cached_mma<32>(a, as_stream(stream));
+        if (d_qk == 64) return run_cached_mma<64>(a, as_stream(stream));
+        return run_cached_mma<128>(a, as_stream(stream));
+    }
     const bool vec = aligned16(k_cache) && k_page_stride % 4 == 0 && k_tok_stride % 4 == 0 &&
                      d_qk % 4 == 0;
-    return vec ? run_cached_simt<float, true>(a, as_stream(stream))
-               : run_cached_simt<float, false>(a, as_stream(stream));
+    return vec ? run_cached_simt<true>(a, as_stream(stream))
+               : run_cached_simt<false>(a, as_stream(stream));
 }
 
 hstu_status_t hstu_quant_groups_w4(const void* W, int64_t ldw, int64_t N, int32_t K, int32_t group,
