@@ -442,8 +442,10 @@ def _launch_on(stream, *ts) -> int:
     """The raw stream of a call whose tensors all live on the current device."""
     dev = torch.cuda.current_device()
     for t in ts:
-        if t is not None and not (t.is_cuda and t.get_device() == dev):
+        if t is not None and t.get_device() != dev:     # -1 for CPU tensors
             raise ValueError("all tensors must be on the current CUDA device")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
     return _stream(stream)
 
 

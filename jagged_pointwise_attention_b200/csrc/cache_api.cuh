@@ -157,6 +157,43 @@ hstu_status_t run_cached_mma(const CachedArgs& a, cudaStream_t stream) {
     }
 }
 
+template <int MT, int NT, int G>
+hstu_status_t launch_linear_w4(const LinearW4Args& a, int warps, cudaStream_t stream) {
+    static int done[kMaxDevices] = {0};
+    constexpr int ring = kW4Stages * w4_stage_bytes<MT>(), sums = 16 * MT * 8 * NT * 4;
+    constexpr int per_warp = ring > sums ? ring : sums;
+    if (!ensure_smem(linear_w4_kernel<MT, NT, G>, 8 * per_warp, done)) return HSTU_ERR_CUDA;
+    const dim3 grid(static_cast<unsigned>((a.N + 16 * MT - 1) / (16 * MT)),
+                    static_cast<unsigned>((a.M + 8 * NT - 1) / (8 * NT)));
+    linear_w4_kernel<MT, NT, G><<<grid, warps * 32, warps * per_warp, stream>>>(a);
+    return launch_status();
+}
+
+template <int MT, int NT>
+hstu_status_t launch_linear_w4_g(const LinearW4Args& a, int warps, cudaStream_t stream) {
+    if (a.G == 32) return launch_linear_w4<MT, NT, 32>(a, warps, stream);
+    if (a.G == 64) return launch_linear_w4<MT, NT, 64>(a, warps, stream);
+    return launch_linear_w4<MT, NT, 128>(a, warps, stream);
+}
+
+// Two row tiles of W a block where they still fill the device twice (x is read
+// half as often), else one; K split over at most eight warps.
+hstu_status_t run_linear_w4(const LinearW4Args& a, cudaStream_t stream) {
+    const int nkb = a.K / 128;
+    const bool wide = a.N >= 2 * 148 * 32;
+    const int most = wide ? 4 : 8, warps = nkb < most ? nkb : most;
+    if (a.M <= 8)
+        return wide ? launch_linear_w4_g<2, 1>(a, warps, stream)
+                    : launch_linear_w4_g<1, 1>(a, warps, stream);
+    if (a.M <= 16)
+        return wide ? launch_linear_w4_g<2, 2>(a, warps, stream)
+                    : launch_linear_w4_g<1, 2>(a, warps, stream);
+    if (a.M <= 32)
+        return wide ? launch_linear_w4_g<2, 4>(a, warps, stream)
+                    : launch_linear_w4_g<1, 4>(a, warps, stream);
+    return launch_linear_w4_g<1, 8>(a, warps, stream);
+}
+
 }  // namespace
 
 extern "C" {
@@ -354,13 +391,8 @@ hstu_status_t hstu_linear_w4_fwd(const void* x, int64_t ldx, int64_t M, int32_t 
                    static_cast<const uint8_t*>(codes), ldc,
                    static_cast<const __nv_bfloat16*>(scales), lds, bias,
                    static_cast<const __nv_bfloat16*>(residual), ldr,
-                   static_cast<__nv_bfloat16*>(y), ldy};
-    const dim3 grid(static_cast<unsigned>((N + 3) / 4), static_cast<unsigned>((M + 7) / 8));
-    cudaStream_t s = as_stream(stream);
-    if (epilogue == HSTU_EPI_SILU) linear_w4_kernel<1><<<grid, 128, 0, s>>>(a);
-    else if (epilogue == HSTU_EPI_RESIDUAL) linear_w4_kernel<2><<<grid, 128, 0, s>>>(a);
-    else linear_w4_kernel<0><<<grid, 128, 0, s>>>(a);
-    return launch_status();
+                   static_cast<__nv_bfloat16*>(y), ldy, static_cast<int>(epilogue)};
+    return run_linear_w4(a, as_stream(stream));
 }
 
 }  // extern "C"

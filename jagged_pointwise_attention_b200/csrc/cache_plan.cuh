@@ -203,12 +203,13 @@ struct CacheAppendArgs {
 constexpr int kAppendWarps = 8;
 
 // Copies rows to their slots, a warp per token: V is the widest type that
-// every address and length is a multiple of.
+// every address and length is a multiple of. Bound by HBM: four vectors a lane
+// are loaded before the first is stored, so 2 KB of a token are in flight.
 template <typename V>
 __global__ void __launch_bounds__(kAppendWarps * 32) cache_append_kernel(const CacheAppendArgs a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int nk = a.k_bytes / static_cast<int>(sizeof(V));
-    const int nv = a.v_bytes / static_cast<int>(sizeof(V));
+    const int n = nk + a.v_bytes / static_cast<int>(sizeof(V));
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * kAppendWarps + warp; t < a.T;
          t += static_cast<int64_t>(gridDim.x) * kAppendWarps) {
         const int64_t slot = a.slots[t];
@@ -218,11 +219,22 @@ __global__ void __launch_bounds__(kAppendWarps * 32) cache_append_kernel(const C
         }
         const int64_t page = slot >> a.shift, row = slot & ((1 << a.shift) - 1);
         const V* ks = reinterpret_cast<const V*>(a.k + t * a.k_stride);
-        const V* vs = reinterpret_cast<const V*>(a.v + t * a.v_stride);
+        const V* vs = reinterpret_cast<const V*>(a.v + t * a.v_stride) - nk;
         V* kd = reinterpret_cast<V*>(a.kc + page * a.kc_page + row * a.kc_tok);
-        V* vd = reinterpret_cast<V*>(a.vc + page * a.vc_page + row * a.vc_tok);
-        for (int i = lane; i < nk; i += 32) kd[i] = ks[i];
-        for (int i = lane; i < nv; i += 32) vd[i] = vs[i];
+        V* vd = reinterpret_cast<V*>(a.vc + page * a.vc_page + row * a.vc_tok) - nk;
+        for (int i0 = lane; i0 < n; i0 += 128) {
+            V f[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = i0 + 32 * u;
+                if (i < n) f[u] = i < nk ? ks[i] : vs[i];
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = i0 + 32 * u;
+                if (i < n) (i < nk ? kd : vd)[i] = f[u];
+            }
+        }
         if (a.ts != nullptr && lane == 0) a.tsc[page * a.tsc_page + row] = a.ts[t];
     }
 }

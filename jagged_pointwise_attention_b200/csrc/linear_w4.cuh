@@ -7,7 +7,7 @@
 #include <cuda_bf16.h>
 
 #include "common.cuh"
-#include "ln_gate.cuh"
+#include "ptx.cuh"
 
 namespace hstu {
 
@@ -24,45 +24,157 @@ struct LinearW4Args {
     int64_t ldr;
     __nv_bfloat16* y;
     int64_t ldy;
+    int epi;                    // 0 none, 1 SiLU, 2 residual
 };
 
-// epilogue: 0 none, 1 SiLU, 2 residual
-template <int EPI>
-__device__ __forceinline__ void w4_store(const LinearW4Args& a, int m, int n, float v) {
+__device__ __forceinline__ void w4_store(const LinearW4Args& a, int64_t m, int n, float v) {
     if (a.bias) v += a.bias[n];
-    if (EPI == 1) v = v / (1.f + __expf(-v));
-    if (EPI == 2) v += __bfloat162float(a.r[m * a.ldr + n]);
+    if (a.epi == 1) v = v / (1.f + __expf(-v));
+    if (a.epi == 2) v += __bfloat162float(a.r[m * a.ldr + n]);
     a.y[m * a.ldy + n] = __float2bfloat16(v);
 }
 
-// One warp per weight row and eight rows of x.
-template <int EPI>
-__global__ void __launch_bounds__(128) linear_w4_kernel(const LinearW4Args a) {
-    const int n = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int m0 = blockIdx.y * 8, mr = min(8, a.M - m0);
-    if (n >= a.N) return;
-    float acc[8] = {};
-    for (int k = lane * 8; k < a.K; k += 256) {
-        const uint32_t c = *reinterpret_cast<const uint32_t*>(a.w + n * a.ldw + k / 2);
-        const float s = __bfloat162float(a.s[n * a.lds + k / a.G]);
-        float w[8];
+// Bound by the codes' bytes. A block takes 16 MT rows of W; its warps split K
+// into contiguous runs of 128-code blocks, so even one row tile spreads over
+// all its bytes, and add their sums in shared memory at the end. Each warp
+// streams its codes through a ring of its own (16-byte cp.async, kW4Stages
+// blocks deep, no barrier of the block), which also frees the mapping of codes
+// to lanes: one 4-byte word is eight consecutive codes, the four lanes of a
+// fragment row hold 32 consecutive ones, so every m16n8k16 product stays inside
+// one scale group whatever its size.
+//
+// Codes become bf16 without a conversion: 0x4300 | c is 128 + c, and minus 136
+// is exact. c - 8 and x are exact bf16, so a group's products and their sum are
+// plain fp32; the scale multiplies the group's sum. The order of k inside a
+// fragment is free as long as W and x share it: nibbles i and i + 4 of a word
+// are one register, and x is paired to match.
+constexpr int kW4Stages = 4;
+constexpr int kW4Pitch = 80;        // bytes of a row in the ring: 64 and 16 against bank conflicts
+
+template <int MT>
+constexpr int w4_stage_bytes() { return 16 * MT * kW4Pitch; }
+
+__device__ __forceinline__ uint32_t w4_pair(uint32_t c, int p) {
+    const uint32_t b = ((c >> (4 * p)) & 0x000f000fu) | 0x43004300u;
+    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&b),
+                                     __floats2bfloat162_rn(136.f, 136.f));
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// MT: 16-row tiles of W a block; NT: 8-row tiles of x a block. G: group size.
+template <int MT, int NT, int G>
+__global__ void __launch_bounds__(256) linear_w4_kernel(const LinearW4Args a) {
+    extern __shared__ __align__(16) uint8_t w4_smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    const int n0 = blockIdx.x * 16 * MT, m0 = blockIdx.y * 8 * NT;
+    const int nkb = a.K / 128;
+    const int kb0 = nkb * warp / warps, kb1 = nkb * (warp + 1) / warps;
+    uint8_t* ring = w4_smem + warp * kW4Stages * w4_stage_bytes<MT>();
+    // copies of a block: lane's 16-byte piece of rows lane / 4, + 8, ...
+    const uint8_t* src[2 * MT];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = (static_cast<int>((c >> (4 * e)) & 15u) - 8) * s;
+    for (int i = 0; i < 2 * MT; ++i)     // rows past N repeat the last one
+        src[i] = a.w + static_cast<int64_t>(min(n0 + 8 * i + g, a.N - 1)) * a.ldw + 16 * t;
+    auto fetch = [&](int kb) {
+        if (kb < kb1) {
+            uint8_t* dst = ring + (kb - kb0) % kW4Stages * w4_stage_bytes<MT>();
 #pragma unroll
-        for (int m = 0; m < 8; ++m) {
-            if (m < mr) {
-                float f[8];
-                unpack8(*reinterpret_cast<const uint4*>(a.x + (m0 + m) * a.ldx + k), f);
+            for (int i = 0; i < 2 * MT; ++i)
+                cp_async16(dst + (8 * i + g) * kW4Pitch + 16 * t, src[i] + static_cast<int64_t>(kb) * 64);
+        }
+        cp_async_commit();
+    };
+    for (int s = 0; s < kW4Stages - 1; ++s) fetch(kb0 + s);
+
+    const __nv_bfloat16* xr[NT];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) acc[m] = fmaf(w[e], f[e], acc[m]);
+    for (int n = 0; n < NT; ++n)         // rows past M repeat the last one
+        xr[n] = a.x + static_cast<int64_t>(min(m0 + 8 * n + g, a.M - 1)) * a.ldx + 8 * t;
+    const __nv_bfloat16* sr[2 * MT];
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i)
+        sr[i] = a.s + static_cast<int64_t>(min(n0 + 8 * i + g, a.N - 1)) * a.lds;
+
+    float acc[MT][NT][4] = {};
+    constexpr int GB = 128 / G;          // groups of a block
+    for (int kb = kb0; kb < kb1; ++kb) {
+        float sc[2 * MT][GB];
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i)
+#pragma unroll
+            for (int q = 0; q < GB; ++q) sc[i][q] = __bfloat162float(__ldg(sr[i] + kb * GB + q));
+        fetch(kb + kW4Stages - 1);
+        cp_async_wait<kW4Stages - 1>();
+        __syncwarp();
+        const uint8_t* st = ring + (kb - kb0) % kW4Stages * w4_stage_bytes<MT>();
+        float sum[MT][NT][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {    // 32 codes: two steps of 16
+            if (j * 32 % G == 0) {
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sum[m][n][e] = 0.f;
+            }
+            uint32_t xb[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(xr[n] + kb * 128 + j * 32));
+                xb[n][0] = __byte_perm(v.x, v.z, 0x5410);
+                xb[n][1] = __byte_perm(v.x, v.z, 0x7632);
+                xb[n][2] = __byte_perm(v.y, v.w, 0x5410);
+                xb[n][3] = __byte_perm(v.y, v.w, 0x7632);
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const uint32_t c0 = *reinterpret_cast<const uint32_t*>(
+                    st + (16 * m + g) * kW4Pitch + 16 * j + 4 * t);
+                const uint32_t c1 = *reinterpret_cast<const uint32_t*>(
+                    st + (16 * m + 8 + g) * kW4Pitch + 16 * j + 4 * t);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t wf[4] = {w4_pair(c0, 2 * h), w4_pair(c1, 2 * h),
+                                            w4_pair(c0, 2 * h + 1), w4_pair(c1, 2 * h + 1)};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        mma_bf16(sum[m][n], wf, xb[n][2 * h], xb[n][2 * h + 1]);
+                }
+            }
+            if ((j + 1) * 32 % G == 0) {
+                constexpr int per = G / 32;
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            acc[m][n][e] = fmaf(sc[2 * m + (e >> 1)][j / per], sum[m][n][e],
+                                                acc[m][n][e]);
             }
         }
+        __syncwarp();                    // the stage is read
     }
+    cp_async_wait<0>();
+    __syncthreads();                     // the rings are free: they hold the warps' sums now
+    constexpr int R = 16 * MT, C = 8 * NT;
+    float* red = reinterpret_cast<float*>(w4_smem);
 #pragma unroll
-    for (int m = 0; m < 8; ++m) {
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) acc[m] += __shfl_xor_sync(0xffffffffu, acc[m], o);
-        if (lane == 0 && m < mr) w4_store<EPI>(a, m0 + m, n, acc[m]);
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                red[(warp * C + 8 * n + 2 * t + (e & 1)) * R + 16 * m + g + 8 * (e >> 1)] = acc[m][n][e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < R * C; i += blockDim.x) {
+        const int r = i % R, c = i / R;
+        if (n0 + r >= a.N || m0 + c >= a.M) continue;
+        float v = 0.f;
+        for (int w = 0; w < warps; ++w) v += red[(w * C + c) * R + r];
+        w4_store(a, m0 + c, n0 + r, v);
     }
 }
 

@@ -123,6 +123,22 @@ __device__ __forceinline__ void cp_async8(void* dst, const void* src) {
                  : "memory");
 }
 
+// The same with 16 bytes, past the L1 cache.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+                 : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// Wait until at most N of this thread's committed groups are in flight.
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Arrive once on `bar` when this thread's cp.async copies so far have landed
 // (the arrival counts towards the barrier's expected count).
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
