@@ -18,8 +18,11 @@
 // bits) to the workspace and a second, small launch adds the parts in line
 // order -- no atomics, the same bits on every run. Every block finds its part
 // by itself: a scan over the B sequence lengths, which costs it about a
-// microsecond and saves a planning launch.
+// microsecond and saves a planning launch; it leaves what it found (a
+// PartHead) for the join.
 #pragma once
+
+#include <cuda_bf16.h>
 
 #include "common.cuh"
 #include "ptx.cuh"
@@ -58,7 +61,17 @@ struct CachedArgs {
     const float* tb;
     int NB;
     float inv_n;
-    float* parts;                   // workspace: two parts a block
+    struct PartHead* heads;         // workspace: one a block
+    float* parts;                   // then two parts a block
+};
+
+// What block c found at the start of its part of the line: the item there.
+struct alignas(16) PartHead {
+    int64_t total;                  // the line's length
+    int64_t start;                  // where the item starts
+    int64_t row;                    // its first row of q and out
+    int32_t tiles;                  // its key tiles; 0: no item starts or goes on here
+    int32_t rows, h, pad;
 };
 
 struct CachedSeq {
@@ -193,40 +206,78 @@ struct Line {
     }
 };
 
+// Called by one thread of every block, also of those without work.
+template <int KT, int NQ>
+__device__ __forceinline__ void write_head(const CachedArgs& a, const LineAt& at, int64_t total,
+                                           int64_t begin) {
+    PartHead p;
+    p.total = total;
+    p.tiles = 0;
+    if (begin < total) {
+        p.start = begin - at.j;
+        p.row = at.s.off + at.qt * NQ;
+        p.tiles = Line<KT, NQ>::tiles(at.s, at.qt);
+        p.rows = min(NQ, at.s.n - at.qt * NQ);
+        p.h = at.h;
+    }
+    a.heads[blockIdx.x] = p;
+}
+
+__device__ __forceinline__ void store_out(float* dst, const float (&v)[1], float f) { *dst = v[0] * f; }
+__device__ __forceinline__ void store_out(__nv_bfloat16* dst, const float (&v)[4], float f) {
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(v[0] * f, v[1] * f),
+                                                pack_bf16x2(v[2] * f, v[3] * f));
+}
+
 // Parts: block c's first item at 2c, its last (when that is another) at 2c + 1,
-// NQ * DV floats each. The join: block c looks at cut c; where that is the
-// first cut inside an item (strictly behind its first tile), it adds the parts
-// of every block that shares the item and writes the item's rows.
-template <int KT, int NQ, typename TOut, int THREADS>
-__global__ void __launch_bounds__(THREADS) attn_cached_join_kernel(const CachedArgs a, int blocks) {
-    __shared__ int64_t scratch[THREADS / 32 + 8];
-    using L = Line<KT, NQ>;
+// NQ * dv floats each. The join: block (c, y) looks at cut c; where that is
+// the first cut inside an item (strictly behind its first tile), it adds the
+// parts of every block that shares the item, V values a thread, and writes
+// them. The y blocks share an item's values.
+constexpr int kJoinThreads = 128;
+
+template <int NQ, int V, typename TOut>
+__global__ void __launch_bounds__(kJoinThreads) attn_cached_join_kernel(const CachedArgs a,
+                                                                        int blocks) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int c = blockIdx.x + 1;           // cuts 1 .. blocks - 1
-    LineAt at;
-    const int64_t total = L::template locate<THREADS>(a, c, blocks, scratch, at, false);
-    const int64_t x = L::cut(total, c, blocks);
-    if (x >= total || at.j == 0) return;
-    const int64_t start = x - at.j, end = start + L::tiles(at.s, at.qt);
-    if (L::cut(total, c - 1, blocks) > start) return;       // an earlier cut lies inside too
+    const PartHead p = a.heads[c];
+    if (p.tiles == 0) return;
+    auto cut = [&](int i) { return p.total * i / blocks; };
+    if (cut(c) == p.start || cut(c - 1) > p.start) return;  // no cut inside, or not its first
+    const int i = (blockIdx.y * kJoinThreads + threadIdx.x) * V;
+    if (i >= p.rows * a.dv) return;
     // Blocks that share the item: c - 1, whose part is its last item's (its
     // only one's when it begins with this item), then c, c + 1, ... while
     // their parts begin inside.
-    const int part_len = NQ * a.dv;
-    const int rows = min(NQ, at.s.n - at.qt * NQ);
-    const int first = 2 * (c - 1) + (L::cut(total, c - 1, blocks) == start ? 0 : 1);
+    const int64_t len = static_cast<int64_t>(NQ) * a.dv, end = p.start + p.tiles;
     int last = c;
-    while (last + 1 < blocks && L::cut(total, last + 1, blocks) < end) ++last;
-    for (int i = threadIdx.x; i < rows * a.dv; i += THREADS) {
-        const int r = i / a.dv, col = i - r * a.dv;
-        float v = a.parts[static_cast<int64_t>(first) * part_len + i];
-        for (int p = c; p <= last; ++p)
-            if (L::cut(total, p, blocks) < L::cut(total, p + 1, blocks))   // empty parts have none
-                v += a.parts[static_cast<int64_t>(2 * p) * part_len + i];
-        TOut* dst = static_cast<TOut*>(a.out) + (at.s.off + at.qt * NQ + r) * a.out_stride +
-                    static_cast<int64_t>(at.h) * a.dv + col;
-        *dst = static_cast<TOut>(v * a.inv_n);
+    while (last + 1 < blocks && cut(last + 1) < end) ++last;
+    const float* src = a.parts + i;
+    float v[V], f[V];
+    auto load = [&](int part, float (&to)[V]) {
+        const float* s = src + part * len;
+        if constexpr (V == 4) {
+            const float4 q = *reinterpret_cast<const float4*>(s);
+            to[0] = q.x, to[1] = q.y, to[2] = q.z, to[3] = q.w;
+        } else {
+            to[0] = *s;
+        }
+    };
+    load(2 * (c - 1) + (cut(c - 1) == p.start ? 0 : 1), v);
+    const bool dense = p.total >= blocks;   // else some blocks have no part
+#pragma unroll 8
+    for (int q = c; q <= last; ++q) {
+        if (dense || cut(q) < cut(q + 1)) {
+            load(2 * q, f);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] += f[e];
+        }
     }
+    const int r = i / a.dv;
+    store_out(static_cast<TOut*>(a.out) + (p.row + r) * a.out_stride +
+                  static_cast<int64_t>(p.h) * a.dv + (i - r * a.dv),
+              v, a.inv_n);
 }
 
 // ------------------------------------------------------------------ the tree

@@ -2,8 +2,8 @@
 // (attn_cached.cuh has the formula and the work line).
 //
 // Bound by the cache's bytes, so the layout serves the loads. Keys come in
-// groups of 16, which never cross a page. Each of a block's eight warps takes
-// every eighth group of the block's part of the line and feeds itself: its
+// groups of 16, which never cross a page. Each of a block's twelve warps takes
+// every twelfth group of the block's part of the line and feeds itself: its
 // lane 0 issues the TMA loads of a group's K and V rows into the warp's own
 // ring, several groups ahead and across item borders, so no barrier of the
 // block stands between two loads and about 192 KB are in flight or in use on
@@ -24,7 +24,7 @@
 
 namespace hstu {
 
-constexpr int kMmaWarps = 8;
+constexpr int kMmaWarps = 12;
 constexpr int kMmaThreads = kMmaWarps * 32;
 constexpr int kMmaKeys = 16;            // keys of a group
 
@@ -36,7 +36,7 @@ struct CachedMmaSmem {
     static constexpr int kBoxBytes = kMmaKeys * kRowBytes;
     static constexpr int kHalfBytes = kBoxes * kBoxBytes;   // K or V of a group
     static constexpr int kStageBytes = 2 * kHalfBytes;
-    static constexpr int kStages = D == 128 ? 3 : 6;
+    static constexpr int kStages = D == 128 ? 2 : 4;
     static constexpr int kPitch = D + 4;                    // of a row of the sums, floats
     // copies of the sums: fewer where a copy is large
     static constexpr int kCopies = NT == 1 ? 4 : NT == 2 ? 2 : 1;
@@ -113,7 +113,9 @@ attn_cached_mma_kernel(const __grid_constant__ CUtensorMap tmK,
     } else {
         const int64_t total = L::template locate<kMmaThreads>(a, blockIdx.x, gridDim.x, scratch, at,
                                                               blockIdx.x == 0);
-        left = L::cut(total, blockIdx.x + 1, gridDim.x) - L::cut(total, blockIdx.x, gridDim.x);
+        const int64_t begin = L::cut(total, blockIdx.x, gridDim.x);
+        left = L::cut(total, blockIdx.x + 1, gridDim.x) - begin;
+        if (tid == 0) write_head<kMmaKeys, NQ>(a, at, total, begin);
     }
     if (left <= 0) return;
 
@@ -187,7 +189,7 @@ attn_cached_mma_kernel(const __grid_constant__ CUtensorMap tmK,
                                   (at.s.off + q0) * a.q_stride + static_cast<int64_t>(at.h) * D;
         __syncthreads();        // the previous item's tables and sums have been read
         if (use_time) {
-            if (tid < NQ) tqs[tid] = tid < rows ? a.ts[at.s.off + q0 + tid] : 0;
+            if (tid < NQ) tqs[tid] = a.ts[at.s.off + q0 + min(tid, rows - 1)];
             if (head_of != at.h && tid >= 64 && tid < 128)
                 tbs[tid - 64] = a.tb[static_cast<int64_t>(at.h) * a.NB + min(tid - 64, a.NB - 1)];
             head_of = at.h;
@@ -222,6 +224,22 @@ attn_cached_mma_kernel(const __grid_constant__ CUtensorMap tmK,
                 pq[n][e] = at.s.ctx + (a.parents != nullptr ? tree.depth[r] : r);
             }
         __syncthreads();
+        // timestamps of the lane's queries: low words, and the item's extremes,
+        // with which a group sees whether its differences fit in 32 bits
+        int tql[NT][2];
+        int64_t tmin = 0, tmax = 0;
+        if (use_time) {
+            tmin = tmax = tqs[0];
+#pragma unroll 1
+            for (int i = 1; i < rows; ++i) {
+                tmin = min(tmin, tqs[i]);
+                tmax = max(tmax, tqs[i]);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) tql[n][e] = static_cast<int>(tqs[8 * n + 2 * t + e]);
+        }
         const float* posh = use_pos ? a.pos + static_cast<int64_t>(at.h) * a.P : nullptr;
         float acc[KS][NT][4];
 #pragma unroll
@@ -289,10 +307,26 @@ attn_cached_mma_kernel(const __grid_constant__ CUtensorMap tmK,
                 }
             }
             // scores to weights
-            int64_t tk[2];
             if (use_time) {
-                tk[0] = tks[stage * kMmaKeys + g];
-                tk[1] = tks[stage * kMmaKeys + g + 8];
+                const int64_t tk0 = tks[stage * kMmaKeys + g], tk1 = tks[stage * kMmaKeys + g + 8];
+                const int64_t lim = int64_t{1} << 31;
+                const bool near = tmax - tk0 < lim && tmax - tk1 < lim && tmin - tk0 > -lim &&
+                                  tmin - tk1 > -lim;
+                if (__all_sync(0xffffffffu, near)) {
+                    const int kl[2] = {static_cast<int>(tk0), static_cast<int>(tk1)};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            x[n][e] += tbs[time_bucket32(tql[n][e & 1] - kl[e >> 1], 31)];
+                } else {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            x[n][e] += tbs[time_bucket64(
+                                tqs[8 * n + 2 * t + (e & 1)] - (e >> 1 ? tk1 : tk0), 63)];
+                }
             }
             uint32_t seen = 0u;         // bit 4n + e: the query sees the key
             uint32_t pf[NT][2];
@@ -302,7 +336,6 @@ attn_cached_mma_kernel(const __grid_constant__ CUtensorMap tmK,
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     float f = s[n][e] + x[n][e];
-                    if (use_time) f += tbs[time_bucket64(tqs[8 * n + 2 * t + (e & 1)] - tk[e >> 1], 63)];
                     bool see = paged;
                     if (tail) {
                         const int m = k0 + g + 8 * (e >> 1) - at.s.ctx;
@@ -321,13 +354,12 @@ attn_cached_mma_kernel(const __grid_constant__ CUtensorMap tmK,
             }
             // O^T += V^T P^T. Rows of V that some query does not see are
             // multiplied by zero, so they have to be finite: rows behind the
-            // sequence are cleared in the fragments, and rows of new tokens
-            // with values that are not finite are cleared and added one by
-            // one to the queries that see them.
-            uint32_t live = 0xffffu;        // keys of the group whose V is used as it is
+            // sequence are cleared, and rows of new tokens with values that
+            // are not finite are added one by one to the queries that see
+            // them and then cleared.
             if (tail) {
                 const int nk = min(kMmaKeys, len - k0);
-                live = (1u << nk) - 1u;
+                uint32_t live = (1u << nk) - 1u;
                 uint32_t odd = 0u;
                 const int r = lane & 15;
                 if (k0 + r >= at.s.ctx && r < nk) {
@@ -376,11 +408,18 @@ attn_cached_mma_kernel(const __grid_constant__ CUtensorMap tmK,
                             }
                     }
                 }
+                __syncwarp();
+                if (live != 0xffffu) {
+                    for (int i = lane; i < S::kHalfBytes / 16; i += 32) {
+                        const int r = i * 16 / S::kRowBytes % kMmaKeys;
+                        if (!((live >> r) & 1u))
+                            *reinterpret_cast<uint4*>(ring + stage * S::kStageBytes + S::kHalfBytes +
+                                                      i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();   // the next TMA copy comes after these stores
+                    __syncwarp();
+                }
             }
-            const uint32_t keep0 = ((live >> (2 * t)) & 1u) * 0xffffu |
-                                   ((live >> (2 * t + 1)) & 1u) * 0xffff0000u;
-            const uint32_t keep1 = ((live >> (2 * t + 8)) & 1u) * 0xffffu |
-                                   ((live >> (2 * t + 9)) & 1u) * 0xffff0000u;
 #pragma unroll
             for (int m = 0; m < KS; ++m) {
                 uint32_t vf[4];
@@ -389,10 +428,6 @@ attn_cached_mma_kernel(const __grid_constant__ CUtensorMap tmK,
                     D >= 64 ? vb + (c >> 3) * S::kBoxBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4)
                             : vb + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
                 ldsm4_t(ad, vf);
-                vf[0] &= keep0;
-                vf[1] &= keep0;
-                vf[2] &= keep1;
-                vf[3] &= keep1;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) mma_bf16(acc[m][n], vf, pf[n][0], pf[n][1]);
             }
@@ -407,17 +442,24 @@ attn_cached_mma_kernel(const __grid_constant__ CUtensorMap tmK,
         for (int r = 0; r < kMmaWarps / S::kCopies; ++r) {
             if (r > 0) __syncthreads();
             if (warp / S::kCopies == r) {
-                float* dst = red + (warp % S::kCopies) * NQ * S::kPitch;
+                float* dst = red + (warp % S::kCopies) * NQ * S::kPitch + 2 * t * S::kPitch + g;
+                // all of a row tile's sums are read before the first is written
 #pragma unroll
-                for (int m = 0; m < KS; ++m)
+                for (int m = 0; m < KS; ++m) {
+                    float old[NT][4];
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float* o = dst + (8 * n + 2 * t + (e & 1)) * S::kPitch + 16 * m + g +
-                                       8 * (e >> 1);
-                            *o = r == 0 ? acc[m][n][e] : *o + acc[m][n][e];
-                        }
+                        for (int e = 0; e < 4; ++e)
+                            old[n][e] = r == 0 ? 0.f
+                                               : dst[(8 * n + (e & 1)) * S::kPitch + 16 * m + 8 * (e >> 1)];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            dst[(8 * n + (e & 1)) * S::kPitch + 16 * m + 8 * (e >> 1)] =
+                                old[n][e] + acc[m][n][e];
+                }
             }
         }
         __syncthreads();

@@ -49,6 +49,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_cached_simt_kernel(const Ca
                                                            blockIdx.x == 0);
     const int64_t begin = L::cut(total, blockIdx.x, gridDim.x);
     int64_t left = L::cut(total, blockIdx.x + 1, gridDim.x) - begin;
+    if (tid == 0) write_head<kSimtKeys, kSimtRows>(a, at, total, begin);
     if (left <= 0) return;
     const float* qp = static_cast<const float*>(a.q);
     const float* kp = static_cast<const float*>(a.k);

@@ -6,6 +6,7 @@
 #include "attn_cached.cuh"
 #include "attn_cached_mma.cuh"
 #include "attn_cached_simt.cuh"
+#include "attn_cached_tc.cuh"
 #include "cache_plan.cuh"
 #include "linear_w4.cuh"
 
@@ -63,19 +64,20 @@ hstu_status_t validate_cached(hstu_dtype_t dtype, const CachedArgs& c, int32_t p
 }
 
 // The join of parts, as a programmatic dependent of the attention launch.
-template <int KT, int NQ, typename TOut>
+template <int NQ, int V, typename TOut>
 hstu_status_t launch_join(const CachedArgs& a, int blocks, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks - 1));
-    cfg.blockDim = dim3(256);
+    constexpr int per = kJoinThreads * V;
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks - 1),
+                       static_cast<unsigned>((NQ * a.dv + per - 1) / per));
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_cached_join_kernel<KT, NQ, TOut, 256>, a,
-                                             blocks);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_cached_join_kernel<NQ, V, TOut>, a, blocks);
     return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }
 
@@ -86,7 +88,7 @@ hstu_status_t launch_cached_simt(const CachedArgs& a, cudaStream_t stream) {
     if (!ensure_smem(attn_cached_simt_kernel<DMAX, VEC>, smem, done)) return HSTU_ERR_CUDA;
     attn_cached_simt_kernel<DMAX, VEC><<<kSimtBlocks, kSimtThreads, smem, stream>>>(a);
     const hstu_status_t st = launch_status();
-    return st == HSTU_OK ? launch_join<kSimtKeys, kSimtRows, float>(a, kSimtBlocks, stream) : st;
+    return st == HSTU_OK ? launch_join<kSimtRows, 1, float>(a, kSimtBlocks, stream) : st;
 }
 
 template <bool VEC>
@@ -97,16 +99,17 @@ hstu_status_t run_cached_simt(const CachedArgs& a, cudaStream_t stream) {
     return launch_cached_simt<128, VEC>(a, stream);
 }
 
-// bf16 [pages, page_size, H d] of a cache, boxes of 16 tokens x 64 (32) columns.
+// bf16 [pages, page_size, H d] of a cache, boxes of `rows` tokens x 64 (32) columns.
 bool make_tmap_cache(CUtensorMap* tm, const void* base, const CachedArgs& a, int64_t page,
-                     int64_t tok) {
+                     int64_t tok, int rows) {
     auto fn = encode_fn();
     if (fn == nullptr) return false;
     const int d = a.dqk;
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.H) * d, cuuint64_t{1} << a.shift,
                           static_cast<cuuint64_t>(a.num_pages)};
     cuuint64_t strides[2] = {static_cast<cuuint64_t>(tok) * 2, static_cast<cuuint64_t>(page) * 2};
-    cuuint32_t box[3] = {static_cast<cuuint32_t>(d >= 64 ? 64 : 32), kMmaKeys, 1};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(d >= 64 ? 64 : 32),
+                         static_cast<cuuint32_t>(rows), 1};
     cuuint32_t estr[3] = {1, 1, 1};
     const CUresult r = fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
                           strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -138,23 +141,48 @@ hstu_status_t launch_cached_mma(const CachedArgs& a, const CUtensorMap& tk, cons
     attn_cached_mma_kernel<D, NT, false>
         <<<kMmaBlocks, kMmaThreads, S::kAlloc, stream>>>(tk, tv, a, qtiles);
     const hstu_status_t st = launch_status();
-    return st == HSTU_OK ? launch_join<kMmaKeys, S::kNQ, __nv_bfloat16>(a, kMmaBlocks, stream) : st;
+    return st == HSTU_OK ? launch_join<S::kNQ, 4, __nv_bfloat16>(a, kMmaBlocks, stream) : st;
 }
 
-// query tiles of 8 NT rows
-int cached_nt(int32_t max_new) { return max_new <= 8 ? 1 : max_new <= 16 ? 2 : 4; }
+template <int D, int NQ>
+hstu_status_t launch_cached_tc(const CachedArgs& a, cudaStream_t stream) {
+    using S = CachedTcSmem<D, NQ>;
+    static int done[kMaxDevices] = {0};
+    CUtensorMap tq, tk, tv;
+    const int page = 1 << a.shift, rows = page < kTcKeys ? page : kTcKeys;
+    if (!make_tmap_cache(&tk, a.k, a, a.k_page, a.k_tok, rows) ||
+        !make_tmap_cache(&tv, a.v, a, a.v_page, a.v_tok, rows) ||
+        !make_tmap_bf16(&tq, a.q, static_cast<uint64_t>(a.H) * D, a.T, a.q_stride * 2, NQ))
+        return HSTU_ERR_CUDA;
+    if (!ensure_smem(attn_cached_tc_kernel<D, NQ>, S::kAlloc, done)) return HSTU_ERR_CUDA;
+    attn_cached_tc_kernel<D, NQ><<<kMmaBlocks, kTcThreads, S::kAlloc, stream>>>(tq, tk, tv, a);
+    const hstu_status_t st = launch_status();
+    return st == HSTU_OK ? launch_join<NQ, 4, __nv_bfloat16>(a, kMmaBlocks, stream) : st;
+}
+
+// Rows of a query tile: up to 16 on warp products (32 for heads of 32, which
+// the tcgen05 kernel does not take), then 64 and 128.
+int cached_rows(int32_t max_new, int32_t d) {
+    if (max_new <= 8) return 8;
+    if (max_new <= 16) return 16;
+    return d == 32 ? 32 : max_new <= 64 ? 64 : 128;
+}
 
 template <int D>
-hstu_status_t run_cached_mma(const CachedArgs& a, cudaStream_t stream) {
-    CUtensorMap tk, tv;
-    if (!make_tmap_cache(&tk, a.k, a, a.k_page, a.k_tok) ||
-        !make_tmap_cache(&tv, a.v, a, a.v_page, a.v_tok))
-        return HSTU_ERR_CUDA;
-    switch (cached_nt(a.max_new)) {
-        case 1: return launch_cached_mma<D, 1>(a, tk, tv, stream);
-        case 2: return launch_cached_mma<D, 2>(a, tk, tv, stream);
-        default: return launch_cached_mma<D, 4>(a, tk, tv, stream);
+hstu_status_t run_cached_bf16(const CachedArgs& a, cudaStream_t stream) {
+    const int rows = cached_rows(a.max_new, D);
+    if constexpr (D != 32) {
+        if (rows == 64) return launch_cached_tc<D, 64>(a, stream);
+        if (rows == 128) return launch_cached_tc<D, 128>(a, stream);
     }
+    CUtensorMap tk, tv;
+    if (!make_tmap_cache(&tk, a.k, a, a.k_page, a.k_tok, kMmaKeys) ||
+        !make_tmap_cache(&tv, a.v, a, a.v_page, a.v_tok, kMmaKeys))
+        return HSTU_ERR_CUDA;
+    if constexpr (D == 32)
+        if (rows == 32) return launch_cached_mma<D, 4>(a, tk, tv, stream);
+    return rows == 8 ? launch_cached_mma<D, 1>(a, tk, tv, stream)
+                     : launch_cached_mma<D, 2>(a, tk, tv, stream);
 }
 
 template <int MT, int NT, int G>
@@ -273,9 +301,9 @@ size_t hstu_attn_cached_workspace_bytes(hstu_dtype_t dtype, int32_t max_new, int
     if ((dtype != HSTU_DTYPE_F32 && dtype != HSTU_DTYPE_BF16) || max_new < 1 || d_v < 1 ||
         d_v > 128)
         return 0;
-    const size_t rows = dtype == HSTU_DTYPE_F32 ? static_cast<size_t>(kSimtBlocks) * kSimtRows
-                                                : static_cast<size_t>(kMmaBlocks) * 8 * cached_nt(max_new);
-    return 2 * rows * d_v * 4;
+    const size_t blocks = dtype == HSTU_DTYPE_F32 ? kSimtBlocks : kMmaBlocks;
+    const size_t rows = dtype == HSTU_DTYPE_F32 ? kSimtRows : cached_rows(max_new, d_v);
+    return blocks * (sizeof(PartHead) + 2 * rows * d_v * 4);
 }
 
 hstu_status_t hstu_attn_cached_fwd(hstu_dtype_t dtype, const void* q, int64_t q_tok_stride,
@@ -328,15 +356,16 @@ hstu_status_t hstu_attn_cached_fwd(hstu_dtype_t dtype, const void* q, int64_t q_
     a.tb = use_time ? time_bias : nullptr;
     a.NB = num_time_buckets;
     a.inv_n = 1.0f / static_cast<float>(max_seqlen);
-    a.parts = static_cast<float*>(workspace);
+    a.heads = static_cast<PartHead*>(workspace);
+    a.parts = reinterpret_cast<float*>(a.heads + (dtype == HSTU_DTYPE_F32 ? kSimtBlocks : kMmaBlocks));
     const hstu_status_t st =
         validate_cached(dtype, a, page_size, workspace, workspace_bytes,
                         hstu_attn_cached_workspace_bytes(dtype, max_new, d_v));
     if (st != HSTU_OK || B == 0 || total_new == 0) return st;
     if (dtype == HSTU_DTYPE_BF16) {
-        if (d_qk == 32) return run_cached_mma<32>(a, as_stream(stream));
-        if (d_qk == 64) return run_cached_mma<64>(a, as_stream(stream));
-        return run_cached_mma<128>(a, as_stream(stream));
+        if (d_qk == 32) return run_cached_bf16<32>(a, as_stream(stream));
+        if (d_qk == 64) return run_cached_bf16<64>(a, as_stream(stream));
+        return run_cached_bf16<128>(a, as_stream(stream));
     }
     const bool vec = aligned16(k_cache) && k_page_stride % 4 == 0 && k_tok_stride % 4 == 0 &&
                      d_qk % 4 == 0;
