@@ -438,72 +438,14 @@ def hstu_attn_bwd_f32(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, dout: t
 # ---------------------------------------------------------------- serving
 
 
-def _launch_on(stream, *ts) -> int:
-    """The raw stream of a call whose tensors all live on the current device."""
-    dev = torch.cuda.current_device()
-    for t in ts:
-        if t is not None and t.get_device() != dev:     # -1 for CPU tensors
-            raise ValueError("all tensors must be on the current CUDA device")
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    return _stream(stream)
+# These calls are short, so their checks and allocations are in C++
+# (csrc/binding.cpp): wrong types raise TypeError, shapes, strides or devices
+# that do not fit raise ValueError, what the library refuses raises HstuError.
+# All tensors must be on the current CUDA device.
 
 
-def _used_on(stream, *ts) -> None:
-    """Tensors allocated by a call and used on another stream than the current
-    one: the allocator must not hand their memory out again before that use."""
-    if stream is None:
-        return
-    s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
-    for t in ts:
-        t.record_stream(s)
-
-
-def _want(t, dtype, what: str, shape=None) -> None:
-    """A contiguous tensor of the given type (and shape)."""
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s" % (what, dtype))
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must have shape %s, got %s" % (what, list(shape), list(t.shape)))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % what)
-
-
-def _cache_strides(t: torch.Tensor, what: str):
-    """(page stride, token stride) of a [num_pages, page_size, H, d] cache."""
-    if t.dim() != 4:
-        raise ValueError("%s must be [num_pages, page_size, H, d]" % what)
-    n, page, H, d = t.shape
-    sp, st, sh, sd = t.stride()
-    if (d > 1 and sd != 1) or (H > 1 and sh != d):
-        raise ValueError("%s: heads and features must be contiguous inside a token" % what)
-    tok = st if page > 1 else H * d
-    return (sp if n > 1 else page * tok), tok
-
-
-def _row_stride(t: torch.Tensor, H: int, d: int) -> int:
-    """_tok_stride where a single token's stride, which means nothing, may be anything."""
-    s = _tok_stride(t, H, d)
-    return s if t.shape[0] > 1 else H * d
-
-
-def _ts_page_stride(ts_cache, num_pages: int, page: int) -> int:
-    if ts_cache is None:
-        return 0
-    if ts_cache.dtype != torch.int64:
-        raise TypeError("ts_cache must be int64")
-    if tuple(ts_cache.shape) != (num_pages, page) or ts_cache.stride(1) != 1:
-        raise ValueError("ts_cache must be [num_pages, page_size] with contiguous pages")
-    return ts_cache.stride(0) if num_pages > 1 else page
-
-
-def _table(block_table: torch.Tensor, B: int):
-    """(row stride, max_pages) of a block table."""
-    if block_table.dtype != torch.int32:
-        raise TypeError("block_table must be int32")
-    if block_table.dim() != 2 or block_table.shape[0] != B or block_table.stride(1) != 1:
-        raise ValueError("block_table must be [B, max_pages] with contiguous rows")
-    return (block_table.stride(0) if B > 1 else block_table.shape[1]), block_table.shape[1]
+def _raw(stream):
+    return None if stream is None else _stream(stream)
 
 
 def hstu_cache_plan(ctx_lens: torch.Tensor, new_offsets: torch.Tensor, free_pages: torch.Tensor,
@@ -518,33 +460,8 @@ def hstu_cache_plan(ctx_lens: torch.Tensor, new_offsets: torch.Tensor, free_page
     (int32 [1]) are taken. Writes the new entries of block_table (int32 [B,
     max_pages]) in place and returns (slots int64 [total_new], free_end int32
     [1], the next step's free_start)."""
-    B = new_offsets.numel() - 1
-    raw = _launch_on(stream, ctx_lens, new_offsets, free_pages, free_start, block_table, slots,
-                     free_end)
-    _want(ctx_lens, torch.int32, "ctx_lens", (B,))
-    _want(new_offsets, torch.int64, "new_offsets")
-    _want(free_pages, torch.int32, "free_pages")
-    _want(free_start, torch.int32, "free_start", (1,))
-    ts, mp = _table(block_table, B)
-    own = []
-    if slots is None:
-        slots = torch.empty(total_new, dtype=torch.int64, device=block_table.device)
-        own.append(slots)
-    else:
-        _want(slots, torch.int64, "slots", (total_new,))
-    if free_end is None:
-        free_end = torch.empty(1, dtype=torch.int32, device=block_table.device)
-        own.append(free_end)
-    else:
-        _want(free_end, torch.int32, "free_end", (1,))
-        if free_end.data_ptr() == free_start.data_ptr():
-            raise ValueError("free_end must not be free_start")
-    _native.check("hstu_cache_plan", _lib().hstu_cache_plan(
-        ctx_lens.data_ptr(), new_offsets.data_ptr(), B, total_new, page_size,
-        free_pages.data_ptr(), free_pages.numel(), free_start.data_ptr(), block_table.data_ptr(),
-        ts, mp, slots.data_ptr(), free_end.data_ptr(), raw))
-    _used_on(stream, *own)
-    return slots, free_end
+    return _native.serving().cache_plan(ctx_lens, new_offsets, free_pages, free_start, block_table,
+                                        page_size, total_new, slots, free_end, _raw(stream))
 
 
 def hstu_cache_append(k: torch.Tensor, v: torch.Tensor, timestamps: Optional[torch.Tensor],
@@ -554,27 +471,7 @@ def hstu_cache_append(k: torch.Tensor, v: torch.Tensor, timestamps: Optional[tor
     any token stride) and timestamps (int64 [T]; given with ts_cache or not at
     all) into the cache at `slots` (int64 [T], all different; negative ones are
     padding and are skipped)."""
-    T, H, dqk = k.shape
-    n, page = k_cache.shape[:2]
-    raw = _launch_on(stream, k, v, timestamps, slots, k_cache, v_cache, ts_cache)
-    if not (k.dtype == v.dtype == k_cache.dtype == v_cache.dtype):
-        raise TypeError("k, v and the caches must share their dtype")
-    dv = v.shape[2]
-    if v.shape[0] != T or tuple(k_cache.shape[2:]) != (H, dqk) or \
-            tuple(v_cache.shape) != (n, page, H, dv):
-        raise ValueError("k, v, k_cache and v_cache do not fit together")
-    _want(slots, torch.int64, "slots", (T,))
-    if timestamps is not None:
-        _want(timestamps, torch.int64, "timestamps", (T,))
-    if (timestamps is None) != (ts_cache is None):
-        raise ValueError("timestamps and ts_cache come together")
-    kp, kt = _cache_strides(k_cache, "k_cache")
-    vp, vt = _cache_strides(v_cache, "v_cache")
-    _native.check("hstu_cache_append", _lib().hstu_cache_append(
-        _dtype_code(k), k.data_ptr(), _row_stride(k, H, dqk), v.data_ptr(), _row_stride(v, H, dv),
-        _ptr(timestamps), slots.data_ptr(), T, H, dqk, dv, k_cache.data_ptr(), kp, kt,
-        v_cache.data_ptr(), vp, vt, _ptr(ts_cache), _ts_page_stride(ts_cache, n, page), n, page,
-        raw))
+    _native.serving().cache_append(k, v, timestamps, slots, k_cache, v_cache, ts_cache, _raw(stream))
 
 
 def hstu_attn_cached_workspace_bytes(dtype: torch.dtype, max_new: int, d_v: int) -> int:
@@ -598,66 +495,15 @@ def hstu_attn_cached_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     follows within its sequence's new tokens, -1: the context; at most 256 new
     tokens a sequence) or None for chains; bias tables as hstu_attn_fwd. A token
     sees the context, its ancestors and itself. Returns out [T, H, d_v]."""
-    T, H, dqk = q.shape
-    n, page = k_cache.shape[:2]
-    dv = v_cache.shape[3]
-    B = new_offsets.numel() - 1
-    raw = _launch_on(stream, q, k_cache, v_cache, ts_cache, block_table, ctx_lens, new_offsets,
-                     timestamps, parents, pos_bias, time_bias, out, workspace)
-    if not (q.dtype == k_cache.dtype == v_cache.dtype):
-        raise TypeError("q and the caches must share their dtype")
-    if tuple(k_cache.shape[2:]) != (H, dqk) or tuple(v_cache.shape[:3]) != (n, page, H):
-        raise ValueError("q, k_cache and v_cache do not fit together")
-    _want(new_offsets, torch.int64, "new_offsets")
-    _want(ctx_lens, torch.int32, "ctx_lens", (B,))
-    if timestamps is not None:
-        _want(timestamps, torch.int64, "timestamps", (T,))
-    if parents is not None:
-        _want(parents, torch.int32, "parents", (T,))
-    for tbl in (pos_bias, time_bias):
-        if tbl is not None:
-            _want(tbl, torch.float32, "bias tables", (H, tbl.shape[-1]))
-    kp, kt = _cache_strides(k_cache, "k_cache")
-    vp, vt = _cache_strides(v_cache, "v_cache")
-    ts, mp = _table(block_table, B)
-    code = _dtype_code(q)
-    own = []
-    if out is None:
-        out = torch.empty((T, H, dv), dtype=q.dtype, device=q.device)
-        own.append(out)
-    elif out.dtype != q.dtype or out.shape[0] != T:
-        raise ValueError("out must be [T, H, d_v] of q's dtype")
-    lib = _lib()
-    if workspace is None:
-        workspace = _workspace(lib.hstu_attn_cached_workspace_bytes(code, max_new, dv), q.device)
-        own.append(workspace)
-    _native.check("hstu_attn_cached_fwd", lib.hstu_attn_cached_fwd(
-        code, q.data_ptr(), _row_stride(q, H, dqk), k_cache.data_ptr(), kp, kt,
-        v_cache.data_ptr(), vp, vt, _ptr(ts_cache), _ts_page_stride(ts_cache, n, page), n, page,
-        block_table.data_ptr(), ts, mp, ctx_lens.data_ptr(), new_offsets.data_ptr(), B, T,
-        max_new, H, dqk, dv, _ptr(timestamps), _ptr(parents), _ptr(pos_bias),
-        0 if pos_bias is None else pos_bias.shape[1], _ptr(time_bias),
-        0 if time_bias is None else time_bias.shape[1], max_seqlen, out.data_ptr(),
-        _row_stride(out, H, dv), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        raw))
-    _used_on(stream, *own)
-    return out
+    return _native.serving().attn_cached(q, k_cache, v_cache, ts_cache, block_table, ctx_lens,
+                                         new_offsets, timestamps, parents, pos_bias, time_bias,
+                                         max_seqlen, max_new, out, workspace, _raw(stream))
 
 
 def hstu_quant_groups_w4(W: torch.Tensor, group: int = 128, stream=None):
     """4-bit codes and group scales of a bf16 [N, K] weight: (codes uint8 [N,
     K/2], scales bf16 [N, K/group]) with W ~ (code - 8) * scale."""
-    raw = _launch_on(stream, W)
-    if W.dtype != torch.bfloat16 or W.dim() != 2 or W.stride(1) != 1:
-        raise ValueError("W must be bf16 [N, K] with unit column stride")
-    N, K = W.shape
-    codes = torch.empty((N, K // 2), dtype=torch.uint8, device=W.device)
-    scales = torch.empty((N, K // group if group > 0 else 0), dtype=torch.bfloat16, device=W.device)
-    _native.check("hstu_quant_groups_w4", _lib().hstu_quant_groups_w4(
-        W.data_ptr(), W.stride(0) if N > 1 else K, N, K, group, codes.data_ptr(), K // 2,
-        scales.data_ptr(), scales.shape[1], raw))
-    _used_on(stream, codes, scales)
-    return codes, scales
+    return _native.serving().quant_w4(W, group, _raw(stream))
 
 
 _EPILOGUES = {"none": _native.HSTU_EPI_NONE, "silu": _native.HSTU_EPI_SILU,
@@ -671,33 +517,5 @@ def hstu_linear_w4_fwd(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tenso
     """epilogue(x W^T + bias) for a few rows, W in 4-bit codes and group scales
     from hstu_quant_groups_w4 (the group is K / scales.shape[1]): "none", "silu"
     or "residual" (adds `residual`). x [M, K] bf16, returns bf16 [M, N]."""
-    raw = _launch_on(stream, x, codes, scales, bias, residual, out)
-    M, K = x.shape
-    N = codes.shape[0]
-    if x.dtype != torch.bfloat16 or (x.stride(1) != 1 and M > 0):
-        raise ValueError("x must be bf16 with unit column stride")
-    if codes.dtype != torch.uint8 or codes.shape[1] * 2 != K or codes.stride(1) != 1:
-        raise ValueError("codes must be uint8 [N, K/2] with unit column stride")
-    ng = scales.shape[1]
-    if scales.dtype != torch.bfloat16 or scales.shape[0] != N or ng < 1 or K % ng or \
-            (ng > 1 and scales.stride(1) != 1):
-        raise ValueError("scales must be bf16 [N, K/group] with unit column stride")
-    if bias is not None:
-        _want(bias, torch.float32, "bias", (N,))
-    own = []
-    if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-        own.append(out)
-    for t, what in ((out, "out"), (residual if epilogue == "residual" else None, "residual")):
-        if t is not None and (t.dtype != torch.bfloat16 or tuple(t.shape) != (M, N)
-                              or (N > 1 and t.stride(1) != 1)):
-            raise ValueError("%s must be bf16 [M, N] with unit column stride" % what)
-    one = M <= 1
-    _native.check("hstu_linear_w4_fwd", _lib().hstu_linear_w4_fwd(
-        x.data_ptr(), K if one else x.stride(0), M, K, codes.data_ptr(),
-        codes.stride(0) if N > 1 else K // 2, scales.data_ptr(),
-        scales.stride(0) if N > 1 else ng, K // ng, N, _ptr(bias), _EPILOGUES[epilogue],
-        _ptr(residual), 0 if residual is None else N if one else residual.stride(0),
-        out.data_ptr(), N if one else out.stride(0), raw))
-    _used_on(stream, *own)
-    return out
+    return _native.serving().linear_w4(x, codes, scales, bias, _EPILOGUES[epilogue], residual, out,
+                                       _raw(stream))

@@ -4,10 +4,13 @@ library cannot be loaded, every call raises."""
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libhstu.so")
+SERVING_PATH = os.path.join(PKG, "_serving.so")
 
 c_i32, c_i64, c_f32, c_sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 c_p = ctypes.c_void_p
@@ -106,6 +109,29 @@ def load(path: str = LIB_PATH):
     if path == LIB_PATH:
         _lib = lib
     return lib
+
+
+_serving = None
+
+
+def serving():
+    """The C++ binding of the serving calls, on the loaded library."""
+    global _serving
+    if _serving is None:
+        if not os.path.exists(SERVING_PATH):
+            raise ImportError("_serving.so is not built (%s); run "
+                              "`python -m jagged_pointwise_attention_b200.build`" % SERVING_PATH)
+        lib = load()
+        loader = importlib.machinery.ExtensionFileLoader(__package__ + "._serving", SERVING_PATH)
+        spec = importlib.util.spec_from_file_location(__package__ + "._serving", SERVING_PATH,
+                                                      loader=loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        module.bind(check, *(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+            "hstu_cache_plan", "hstu_cache_append", "hstu_attn_cached_workspace_bytes",
+            "hstu_attn_cached_fwd", "hstu_quant_groups_w4", "hstu_linear_w4_fwd")))
+        _serving = module
+    return _serving
 
 
 def check(fn_name: str, status: int) -> None:

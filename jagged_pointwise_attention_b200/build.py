@@ -1,4 +1,5 @@
-"""Build libhstu.so in-tree with nvcc for sm_100a.
+"""Build libhstu.so in-tree with nvcc for sm_100a, and _serving.so, the Python
+binding of the serving calls, with g++.
 
     python -m jagged_pointwise_attention_b200.build [--force] [--verbose]
 
@@ -14,12 +15,15 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libhstu.so")
+BINDING = os.path.join(PKG, "_serving.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -41,7 +45,31 @@ def needs_build(out: str = LIB) -> bool:
     return any(os.path.getmtime(s) > t for s in _sources())
 
 
+def build_binding(force: bool = False) -> str:
+    """_serving.so against the installed torch (its headers, its C++ ABI)."""
+    newest = max(os.path.getmtime(BINDING_SRC), os.path.getmtime(os.path.join(INCLUDE, "hstu.h")))
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+        return BINDING
+    import torch
+
+    tdir = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    tmp = BINDING + ".tmp.%d" % os.getpid()
+    subprocess.check_call([
+        os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+        "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+        "-I", INCLUDE, "-isystem", os.path.join(tdir, "include"),
+        "-isystem", os.path.join(tdir, "include", "torch", "csrc", "api", "include"),
+        "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"),
+        "-o", tmp, BINDING_SRC, "-L", os.path.join(tdir, "lib"),
+        "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"])
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, out: str = LIB, extra=()) -> str:
+    if out == LIB:
+        build_binding(force)
     if not force and not needs_build(out):
         return out
     nvcc = os.environ.get("NVCC", "nvcc")
