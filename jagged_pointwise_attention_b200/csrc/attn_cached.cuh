@@ -29,6 +29,28 @@
 
 namespace hstu {
 
+// x / (1 + exp(-x)) by exp2 and a reciprocal, both to a few units in the last
+// place of 32 bits. (The approximate tanh of the dense forward is off by more
+// than a bf16 step of silu for scores below about -3.) Very negative x: the
+// exponential overflows to infinity, its reciprocal is 0.
+__device__ __forceinline__ float silu_exp(float x) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return x * r;
+}
+
+// Byte offset of the bucket floor(log2(max(1, dt))) in a table of floats that
+// starts kBucketBias bytes earlier: the exponent of dt as a float, rounded
+// towards zero so that it never carries into the next power of two.
+constexpr int kBucketBias = 127 * 4;
+__device__ __forceinline__ uint32_t bucket_bytes(int dt) {
+    return (__float_as_uint(__int2float_rz(max(dt, 1))) >> 21) & 0x7fcu;
+}
+__device__ __forceinline__ float table_at(const float* base, uint32_t bytes) {
+    return *reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(base) + bytes);
+}
+
 constexpr int kMaxTree = 256;       // new tokens of a sequence that come as a tree
 
 struct CachedArgs {
@@ -251,8 +273,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_cached_join_kernel(const Ca
     // only one's when it begins with this item), then c, c + 1, ... while
     // their parts begin inside.
     const int64_t len = static_cast<int64_t>(NQ) * a.dv, end = p.start + p.tiles;
-    int last = c;
-    while (last + 1 < blocks && cut(last + 1) < end) ++last;
+    const int last = min(blocks - 1, static_cast<int>((end * blocks - 1) / p.total));  // cut(last) < end
     const float* src = a.parts + i;
     float v[V], f[V];
     auto load = [&](int part, float (&to)[V]) {

@@ -15,60 +15,55 @@
 // P^T comes out of the first product's layout by one 8 x 8 transpose a tile
 // (movmatrix). The tensor pipe idles either way: a 128-wide tcgen05 tile would
 // hold one query here and put TMEM and its barriers on the path of each group.
-//
-// silu by exp2 and a reciprocal: the approximate tanh that the dense forward
-// uses is off by more than a bf16 step of silu for scores below about -3.
 #pragma once
 
 #include "attn_cached.cuh"
 
 namespace hstu {
 
-constexpr int kMmaWarps = 12;
-constexpr int kMmaThreads = kMmaWarps * 32;
 constexpr int kMmaKeys = 16;            // keys of a group
 
-template <int D, int NT>
+template <int D, int NT, bool WHOLE>
 struct CachedMmaSmem {
+    // Whole items: four warps, so that three blocks share an SM.
+    static constexpr int kWarps = WHOLE ? 4 : 12;
+    static constexpr int kThreads = kWarps * 32;
     static constexpr int kNQ = 8 * NT;
     static constexpr int kRowBytes = D >= 64 ? 128 : 64;    // bytes of a box row
     static constexpr int kBoxes = D / 64 > 0 ? D / 64 : 1;
     static constexpr int kBoxBytes = kMmaKeys * kRowBytes;
     static constexpr int kHalfBytes = kBoxes * kBoxBytes;   // K or V of a group
     static constexpr int kStageBytes = 2 * kHalfBytes;
-    static constexpr int kStages = D == 128 ? 2 : 4;
+    static constexpr int kStages = D == 128 || WHOLE ? 2 : 4;
     static constexpr int kPitch = D + 4;                    // of a row of the sums, floats
     // copies of the sums: fewer where a copy is large
     static constexpr int kCopies = NT == 1 ? 4 : NT == 2 ? 2 : 1;
-    static constexpr int kOffRed = kMmaWarps * kStages * kStageBytes;
+    static constexpr int kOffRed = kWarps * kStages * kStageBytes;
     static constexpr int kOffQ = kOffRed;                   // NT > 2: until the sums come
     static constexpr int kQPitch = D * 2 + 16;
     static constexpr int kOffTk = kOffRed + kCopies * kNQ * kPitch * 4;    // [warp][stage][16]
-    static constexpr int kOffTq = kOffTk + kMmaWarps * kStages * kMmaKeys * 8;
+    static constexpr int kOffTq = kOffTk + kWarps * kStages * kMmaKeys * 8;
     static constexpr int kOffTb = kOffTq + kNQ * 8;
     static constexpr int kOffBar = kOffTb + 64 * 4;
-    static constexpr int kOffPage = kOffBar + kMmaWarps * kStages * 8;
-    static constexpr int kOffScratch = kOffPage + kMmaWarps * kStages * 4;
-    static constexpr int kOffTree = (kOffScratch + (kMmaWarps + 8) * 8 + 15) / 16 * 16;
+    static constexpr int kOffPage = kOffBar + kWarps * kStages * 8;
+    static constexpr int kOffScratch = kOffPage + kWarps * kStages * 4;
+    static constexpr int kOffTree = (kOffScratch + (kWarps + 8) * 8 + 15) / 16 * 16;
     static constexpr int kOffAbort = kOffTree + static_cast<int>(sizeof(TreeSmem));
     static constexpr int kBytes = kOffAbort + 16;
     static constexpr int kAlloc = kBytes + 1024;
     static_assert(kAlloc <= 227 * 1024, "shared memory per block");
 };
 
-__device__ __forceinline__ float silu_exp(float x) {
-    return __fdividef(x, 1.f + exp2f(-1.4426950408889634f * x));
-}
-
 // WHOLE: block i takes item i whole (short sequences: no part, no join, no
 // search); otherwise an equal part of the line.
 template <int D, int NT, bool WHOLE>
-__global__ void __launch_bounds__(kMmaThreads, 1)
+__global__ void __launch_bounds__(CachedMmaSmem<D, NT, WHOLE>::kThreads, WHOLE ? 3 : 1)
 attn_cached_mma_kernel(const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const CachedArgs a, int qtiles) {
-    using S = CachedMmaSmem<D, NT>;
+    using S = CachedMmaSmem<D, NT, WHOLE>;
     using L = Line<kMmaKeys, S::kNQ>;
     constexpr int NQ = S::kNQ, ST = S::kStages, KS = D / 16;
+    constexpr int kMmaWarps = S::kWarps, kMmaThreads = S::kThreads;
     constexpr bool kQRegs = NT <= 2;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -267,7 +262,8 @@ attn_cached_mma_kernel(const __grid_constant__ CUtensorMap tmK,
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int rel = max(0, min(pq[n][e & 1] - pk[e >> 1], a.P - 1));
+                    int rel = min(pq[n][e & 1] - pk[e >> 1], a.P - 1);
+                    if (tail) rel = max(rel, 0);    // a new token that is not seen
                     x[n][e] = use_pos ? __ldg(posh + rel) : 0.f;
                 }
             if (!failed && !warp_wait(&full[stage], phase, abort_flag)) {
@@ -318,7 +314,7 @@ attn_cached_mma_kernel(const __grid_constant__ CUtensorMap tmK,
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            x[n][e] += tbs[time_bucket32(tql[n][e & 1] - kl[e >> 1], 31)];
+                            x[n][e] += table_at(tbs, bucket_bytes(tql[n][e & 1] - kl[e >> 1]) - kBucketBias);
                 } else {
 #pragma unroll
                     for (int n = 0; n < NT; ++n)

@@ -43,7 +43,7 @@ struct CachedTcSmem {
     static constexpr int kOffWin = kOffP + 2 * kPBytes;     // [group][parity][kWin]
     static constexpr int kOffTq = kOffWin + 4 * kWin * 4;   // int64 [NQ]
     static constexpr int kOffTql = kOffTq + NQ * 8;         // their low words
-    static constexpr int kOffQo = kOffTql + NQ * 4;         // position behind the tile's lowest
+    static constexpr int kOffQo = kOffTql + NQ * 4;         // 4 x position behind the tile's lowest
     static constexpr int kOffTb = kOffQo + NQ * 4;
     static constexpr int kOffBar = kOffTb + 64 * 4;
     static constexpr int kOffScratch = kOffBar + 64 * 8;
@@ -330,7 +330,7 @@ attn_cached_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
             }
             if (tid < NQ) {
                 const int m = min(tid, rows - 1);
-                qos[tid] = chain ? m : tree.depth[q0 + m];
+                qos[tid] = 4 * (chain ? m : tree.depth[q0 + m]);
                 if (use_time) {
                     tqs[tid] = a.ts[I.s.off + q0 + m];
                     tql[tid] = static_cast<int>(tqs[tid]);
@@ -367,7 +367,7 @@ attn_cached_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
             // keys from here on are seen by some queries and not by others
             const int part0 = pbase;
             const float* posh = use_pos ? a.pos + static_cast<int64_t>(I.h) * a.P : nullptr;
-            const int span = q_span[0];
+            const int span = q_span[0] / 4;
             // this thread's key of a step: its page (-1: none) and timestamp
             auto key_of = [&](int j, int& page) {
                 const int key = (I.j + j) * kTcKeys + r;
@@ -419,28 +419,37 @@ attn_cached_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                     float x[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(sv[e]);
+                    int qo[16];
+                    if (use_pos && !(fast && chain)) {
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4)
+                            *reinterpret_cast<int4*>(qo + e) =
+                                *reinterpret_cast<const int4*>(qos + c0 + e);
+                    }
                     if (use_pos) {
-                        if (fast) {
-                            // qos is the query's own index in a chain
-                            // (entries behind the last query's belong to columns nobody reads)
-                            if (chain) {
+                        // (entries behind the last query's belong to columns nobody reads)
+                        if (fast && chain) {
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) x[e] += wr[c0 + e];
-                            } else {
+                            for (int e = 0; e < 16; ++e) x[e] += wr[c0 + e];
+                        } else if (fast) {
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) x[e] += wr[qos[c0 + e]];
-                            }
+                            for (int e = 0; e < 16; ++e) x[e] += table_at(wr, qo[e]);
                         } else {
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
-                                x[e] += __ldg(posh + max(0, min(pbase + qos[c0 + e] - pk, a.P - 1)));
+                                x[e] += __ldg(posh + max(0, min(pbase + qo[e] / 4 - pk, a.P - 1)));
                         }
                     }
                     if (use_time) {
                         if (near) {
 #pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                x[e] += tbs[time_bucket32(tql[c0 + e] - tkl, 31)];
+                            for (int e = 0; e < 16; e += 4) {
+                                const int4 tq = *reinterpret_cast<const int4*>(tql + c0 + e);
+                                x[e] += table_at(tbs, bucket_bytes(tq.x - tkl) - kBucketBias);
+                                x[e + 1] += table_at(tbs, bucket_bytes(tq.y - tkl) - kBucketBias);
+                                x[e + 2] += table_at(tbs, bucket_bytes(tq.z - tkl) - kBucketBias);
+                                x[e + 3] += table_at(tbs, bucket_bytes(tq.w - tkl) - kBucketBias);
+                            }
                         } else {
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
@@ -459,10 +468,13 @@ attn_cached_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                     if (!paged) seen = 0u;
                     uint32_t pk2[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float p0 = silu_exp(x[2 * e]), p1 = silu_exp(x[2 * e + 1]);
-                        pk2[e] = pack_bf16x2((seen >> (2 * e)) & 1u ? p0 : 0.f,
-                                             (seen >> (2 * e + 1)) & 1u ? p1 : 0.f);
+                    for (int e = 0; e < 8; ++e)
+                        pk2[e] = pack_bf16x2(silu_exp(x[2 * e]), silu_exp(x[2 * e + 1]));
+                    if (seen != 0xffffu) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            pk2[e] &= ((seen >> (2 * e)) & 1u) * 0xffffu |
+                                      ((seen >> (2 * e + 1)) & 1u) * 0xffff0000u;
                     }
                     // 64 queries a 128-byte row, 16-byte pieces in the 128-byte swizzle
                     const uint32_t base = smem_u32(prow) + (c0 >> 6) * 16384;
@@ -538,7 +550,7 @@ attn_cached_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                                                    (key >> a.shift)];
                             const int row = key & ((1 << a.shift) - 1);
                             const float p = cached_weight<D>(
-                                a, I, I.s.off + qi, pbase + qos[r],
+                                a, I, I.s.off + qi, pbase + qos[r] / 4,
                                 chain ? key : I.s.ctx + tree.depth[m], use_time ? tqs[r] : 0,
                                 static_cast<const __nv_bfloat16*>(a.k) + pg * a.k_page + row * a.k_tok +
                                     static_cast<int64_t>(I.h) * D,

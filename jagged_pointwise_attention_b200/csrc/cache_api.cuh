@@ -119,29 +119,31 @@ bool make_tmap_cache(CUtensorMap* tm, const void* base, const CachedArgs& a, int
 }
 
 constexpr int kMmaBlocks = 148;
-// Sequences up to this length are taken whole by a block each: at most eight
-// groups a warp, less than the search of the line and the join cost.
+// Sequences up to this length are taken whole by a block each: at most sixteen
+// groups a warp, about what the search of the line and the join cost.
 constexpr int kWholeLen = 1024;
 
 template <int D, int NT>
 hstu_status_t launch_cached_mma(const CachedArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
                                 cudaStream_t stream) {
-    using S = CachedMmaSmem<D, NT>;
-    const int qtiles = (a.max_new + S::kNQ - 1) / S::kNQ;
+    constexpr int NQ = 8 * NT;
+    const int qtiles = (a.max_new + NQ - 1) / NQ;
     const int64_t items = static_cast<int64_t>(a.B) * qtiles * a.H;
     if (a.max_seqlen <= kWholeLen && items <= 0x7fffffff) {
+        using S = CachedMmaSmem<D, NT, true>;
         static int done[kMaxDevices] = {0};
         if (!ensure_smem(attn_cached_mma_kernel<D, NT, true>, S::kAlloc, done)) return HSTU_ERR_CUDA;
         attn_cached_mma_kernel<D, NT, true>
-            <<<static_cast<unsigned>(items), kMmaThreads, S::kAlloc, stream>>>(tk, tv, a, qtiles);
+            <<<static_cast<unsigned>(items), S::kThreads, S::kAlloc, stream>>>(tk, tv, a, qtiles);
         return launch_status();
     }
+    using S = CachedMmaSmem<D, NT, false>;
     static int done[kMaxDevices] = {0};
     if (!ensure_smem(attn_cached_mma_kernel<D, NT, false>, S::kAlloc, done)) return HSTU_ERR_CUDA;
     attn_cached_mma_kernel<D, NT, false>
-        <<<kMmaBlocks, kMmaThreads, S::kAlloc, stream>>>(tk, tv, a, qtiles);
+        <<<kMmaBlocks, S::kThreads, S::kAlloc, stream>>>(tk, tv, a, qtiles);
     const hstu_status_t st = launch_status();
-    return st == HSTU_OK ? launch_join<S::kNQ, 4, __nv_bfloat16>(a, kMmaBlocks, stream) : st;
+    return st == HSTU_OK ? launch_join<NQ, 4, __nv_bfloat16>(a, kMmaBlocks, stream) : st;
 }
 
 template <int D, int NQ>

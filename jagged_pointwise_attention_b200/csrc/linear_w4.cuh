@@ -96,14 +96,41 @@ __global__ void __launch_bounds__(256) linear_w4_kernel(const LinearW4Args a) {
     for (int i = 0; i < 2 * MT; ++i)
         sr[i] = a.s + static_cast<int64_t>(min(n0 + 8 * i + g, a.N - 1)) * a.lds;
 
-    float acc[MT][NT][4] = {};
+    // x and the scales are loaded a block ahead (x while that costs few registers)
     constexpr int GB = 128 / G;          // groups of a block
+    constexpr bool kAhead = NT <= 2;
+    uint4 xn[kAhead ? NT : 1][4];
+    __nv_bfloat16 sn[2 * MT][GB];
+    auto ahead = [&](int kb) {
+        if (kb >= kb1) return;
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i)
+#pragma unroll
+            for (int q = 0; q < GB; ++q) sn[i][q] = __ldg(sr[i] + kb * GB + q);
+        if (kAhead) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    xn[n][j] = ldg_nc_v4(xr[n] + kb * 128 + j * 32);
+        }
+    };
+    ahead(kb0);
+    float acc[MT][NT][4] = {};
     for (int kb = kb0; kb < kb1; ++kb) {
         float sc[2 * MT][GB];
 #pragma unroll
         for (int i = 0; i < 2 * MT; ++i)
 #pragma unroll
-            for (int q = 0; q < GB; ++q) sc[i][q] = __bfloat162float(__ldg(sr[i] + kb * GB + q));
+            for (int q = 0; q < GB; ++q) sc[i][q] = __bfloat162float(sn[i][q]);
+        uint4 xc[kAhead ? NT : 1][4];
+        if (kAhead) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) xc[n][j] = xn[n][j];
+        }
+        ahead(kb + 1);
         fetch(kb + kW4Stages - 1);
         cp_async_wait<kW4Stages - 1>();
         __syncwarp();
@@ -122,7 +149,8 @@ __global__ void __launch_bounds__(256) linear_w4_kernel(const LinearW4Args a) {
             uint32_t xb[NT][4];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(xr[n] + kb * 128 + j * 32));
+                const uint4 v = kAhead ? xc[kAhead ? n : 0][j]
+                                       : __ldg(reinterpret_cast<const uint4*>(xr[n] + kb * 128 + j * 32));
                 xb[n][0] = __byte_perm(v.x, v.z, 0x5410);
                 xb[n][1] = __byte_perm(v.x, v.z, 0x7632);
                 xb[n][2] = __byte_perm(v.y, v.w, 0x5410);
