@@ -193,8 +193,8 @@ struct Line {
             int64_t* f = scratch + THREADS / 32;
             f[0] = b;
             f[1] = qt;
-            f[2] = r / nt;
-            f[3] = r % nt;
+            f[2] = static_cast<uint32_t>(r) / static_cast<uint32_t>(nt);   // r < tiles * H < 2^32
+            f[3] = static_cast<uint32_t>(r) % static_cast<uint32_t>(nt);
             f[4] = s.off;
             f[5] = s.ctx;
             f[6] = s.n;
@@ -286,10 +286,27 @@ __global__ void __launch_bounds__(kJoinThreads) attn_cached_join_kernel(const Ca
         }
     };
     load(2 * (c - 1) + (cut(c - 1) == p.start ? 0 : 1), v);
-    const bool dense = p.total >= blocks;   // else some blocks have no part
-#pragma unroll 8
-    for (int q = c; q <= last; ++q) {
-        if (dense || cut(q) < cut(q + 1)) {
+    if (p.total >= blocks) {
+        // every block has a part; eight loads at a time
+        int q = c;
+        for (; q + 8 <= last + 1; q += 8) {
+            float w[8][V];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) load(2 * (q + u), w[u]);
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+#pragma unroll
+                for (int e = 0; e < V; ++e) v[e] += w[u][e];
+        }
+        for (; q <= last; ++q) {
+            load(2 * q, f);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] += f[e];
+        }
+    } else {
+        // fewer tiles than blocks: a block has one or none
+        for (int q = c; q <= last; ++q) {
+            if (cut(q) == cut(q + 1)) continue;
             load(2 * q, f);
 #pragma unroll
             for (int e = 0; e < V; ++e) v[e] += f[e];

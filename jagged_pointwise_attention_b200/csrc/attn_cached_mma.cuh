@@ -66,8 +66,8 @@ attn_cached_mma_kernel(const __grid_constant__ CUtensorMap tmK,
     constexpr int kMmaWarps = S::kWarps, kMmaThreads = S::kThreads;
     constexpr bool kQRegs = NT <= 2;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    // (an offset, not a rounded address: the compiler keeps seeing shared memory)
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;      // fragment row, column pair
     uint8_t* ring = smem + warp * ST * S::kStageBytes;

@@ -58,14 +58,15 @@ struct CachedTcSmem {
 // A key's contribution to one query, alone: the rare keys whose values are not
 // finite and which some query of the tile does not see.
 template <int D>
-__device__ __noinline__ float cached_weight(const CachedArgs& a, const LineAt& at, int64_t qrow,
-                                            int pq, int pk, int64_t tq, const __nv_bfloat16* krow,
-                                            int64_t tk, const float* tbs) {
+__device__ __forceinline__ float cached_weight(const CachedArgs& a, int h, int64_t qrow, int pq,
+                                               int pk, int64_t tq, const __nv_bfloat16* krow,
+                                               int64_t tk, const float* tbs) {
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + qrow * a.q_stride +
-                             static_cast<int64_t>(at.h) * D;
+                             static_cast<int64_t>(h) * D;
     float s = 0.f;
+#pragma unroll 1
     for (int c = 0; c < D; ++c) s = fmaf(__bfloat162float(q[c]), __bfloat162float(krow[c]), s);
-    if (a.pos) s += a.pos[static_cast<int64_t>(at.h) * a.P + min(pq - pk, a.P - 1)];
+    if (a.pos) s += a.pos[static_cast<int64_t>(h) * a.P + min(pq - pk, a.P - 1)];
     if (a.tsc) s += tbs[time_bucket64(tq - tk, 63)];
     return silu_exp(s);
 }
@@ -79,8 +80,8 @@ attn_cached_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
     using L = Line<kTcKeys, NQ>;
     constexpr int NS = S::kSlots;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    // (an offset, not a rounded address: the compiler keeps seeing shared memory)
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int64_t* tqs = reinterpret_cast<int64_t*>(smem + S::kOffTq);
     int* tql = reinterpret_cast<int*>(smem + S::kOffTql);
@@ -419,25 +420,24 @@ attn_cached_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                     float x[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(sv[e]);
-                    int qo[16];
-                    if (use_pos && !(fast && chain)) {
-#pragma unroll
-                        for (int e = 0; e < 16; e += 4)
-                            *reinterpret_cast<int4*>(qo + e) =
-                                *reinterpret_cast<const int4*>(qos + c0 + e);
-                    }
+                    // (entries behind the last query's belong to columns nobody reads)
                     if (use_pos) {
-                        // (entries behind the last query's belong to columns nobody reads)
                         if (fast && chain) {
 #pragma unroll
                             for (int e = 0; e < 16; ++e) x[e] += wr[c0 + e];
                         } else if (fast) {
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) x[e] += table_at(wr, qo[e]);
+                            for (int e = 0; e < 16; e += 4) {
+                                const int4 qo = *reinterpret_cast<const int4*>(qos + c0 + e);
+                                x[e] += table_at(wr, qo.x);
+                                x[e + 1] += table_at(wr, qo.y);
+                                x[e + 2] += table_at(wr, qo.z);
+                                x[e + 3] += table_at(wr, qo.w);
+                            }
                         } else {
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
-                                x[e] += __ldg(posh + max(0, min(pbase + qo[e] / 4 - pk, a.P - 1)));
+                                x[e] += __ldg(posh + max(0, min(pbase + qos[c0 + e] / 4 - pk, a.P - 1)));
                         }
                     }
                     if (use_time) {
@@ -550,7 +550,7 @@ attn_cached_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                                                    (key >> a.shift)];
                             const int row = key & ((1 << a.shift) - 1);
                             const float p = cached_weight<D>(
-                                a, I, I.s.off + qi, pbase + qos[r] / 4,
+                                a, I.h, I.s.off + qi, pbase + qos[r] / 4,
                                 chain ? key : I.s.ctx + tree.depth[m], use_time ? tqs[r] : 0,
                                 static_cast<const __nv_bfloat16*>(a.k) + pg * a.k_page + row * a.k_tok +
                                     static_cast<int64_t>(I.h) * D,
