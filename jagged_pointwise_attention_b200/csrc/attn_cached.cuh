@@ -123,6 +123,14 @@ struct LineAt {
     CachedSeq s;
 };
 
+// Where block c's part of a line begins (0 <= c <= blocks < 1024). Short lines
+// spare the 64-bit division.
+__device__ __forceinline__ int64_t line_cut(int64_t total, int c, int blocks) {
+    if (total < (1 << 22))
+        return static_cast<uint32_t>(total) * static_cast<uint32_t>(c) / static_cast<uint32_t>(blocks);
+    return total * c / blocks;
+}
+
 template <int KT, int NQ>
 struct Line {
     static __device__ __forceinline__ int tiles(const CachedSeq& s, int qt) {
@@ -135,7 +143,7 @@ struct Line {
         return w;
     }
     static __device__ __forceinline__ int64_t cut(int64_t total, int c, int blocks) {
-        return total * c / blocks;
+        return line_cut(total, c, blocks);
     }
 
     // Block-wide: finds the line's length and the position of cut c. THREADS
@@ -252,70 +260,107 @@ __device__ __forceinline__ void store_out(__nv_bfloat16* dst, const float (&v)[4
 }
 
 // Parts: block c's first item at 2c, its last (when that is another) at 2c + 1,
-// NQ * dv floats each. The join: block (c, y) looks at cut c; where that is
-// the first cut inside an item (strictly behind its first tile), it adds the
-// parts of every block that shares the item, V values a thread, and writes
-// them. The y blocks share an item's values.
-constexpr int kJoinThreads = 128;
+// NQ * dv floats each. An item is shared where a cut lies strictly behind its
+// first tile; the first such cut stands for it. Every block of the join reads
+// all heads at once and lists the shared items, those of up to kJoinFew parts
+// and those of more, and takes every gridDim-th unit of work: of the former
+// 32 V values a warp, of the latter 32 V values, of which each warp adds an
+// eighth of the parts and one the eight sums. The order of the sums is fixed
+// by the lengths.
+constexpr int kJoinWarps = 8;
+constexpr int kJoinThreads = kJoinWarps * 32;
+constexpr int kJoinBlocks = 3 * 148;
+constexpr int kJoinFew = 6;
 
-template <int NQ, int V, typename TOut>
-__global__ void __launch_bounds__(kJoinThreads) attn_cached_join_kernel(const CachedArgs a,
-                                                                        int blocks) {
+template <int NQ, int V, typename TOut, int BLOCKS>
+__global__ void __launch_bounds__(kJoinThreads) attn_cached_join_kernel(const CachedArgs a) {
+    __shared__ int cuts[2][BLOCKS];             // few, many
+    __shared__ int warp_n[2][kJoinWarps];
+    __shared__ float sums[kJoinWarps][32 * V];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int c = blockIdx.x + 1;           // cuts 1 .. blocks - 1
-    const PartHead p = a.heads[c];
-    if (p.tiles == 0) return;
-    auto cut = [&](int i) { return p.total * i / blocks; };
-    if (cut(c) == p.start || cut(c - 1) > p.start) return;  // no cut inside, or not its first
-    const int i = (blockIdx.y * kJoinThreads + threadIdx.x) * V;
-    if (i >= p.rows * a.dv) return;
-    // Blocks that share the item: c - 1, whose part is its last item's (its
-    // only one's when it begins with this item), then c, c + 1, ... while
-    // their parts begin inside.
-    const int64_t len = static_cast<int64_t>(NQ) * a.dv, end = p.start + p.tiles;
-    const int last = min(blocks - 1, static_cast<int>((end * blocks - 1) / p.total));  // cut(last) < end
-    const float* src = a.parts + i;
-    float v[V], f[V];
-    auto load = [&](int part, float (&to)[V]) {
-        const float* s = src + part * len;
-        if constexpr (V == 4) {
-            const float4 q = *reinterpret_cast<const float4*>(s);
-            to[0] = q.x, to[1] = q.y, to[2] = q.z, to[3] = q.w;
-        } else {
-            to[0] = *s;
-        }
+    const int64_t total = a.heads[0].total;
+    // blocks that share the item at cut c: c - 1 .. this one
+    auto last_of = [&](const PartHead& p) {
+        return min(BLOCKS - 1, static_cast<int>(((p.start + p.tiles) * BLOCKS - 1) / total));
     };
-    load(2 * (c - 1) + (cut(c - 1) == p.start ? 0 : 1), v);
-    if (p.total >= blocks) {
-        // every block has a part; eight loads at a time
-        int q = c;
-        for (; q + 8 <= last + 1; q += 8) {
-            float w[8][V];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) load(2 * (q + u), w[u]);
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-#pragma unroll
-                for (int e = 0; e < V; ++e) v[e] += w[u][e];
+    int n[2] = {0, 0};
+    for (int c0 = 1; c0 < BLOCKS; c0 += kJoinThreads) {
+        const int c = c0 + tid;
+        bool is = false, many = false;
+        if (c < BLOCKS) {
+            const PartHead p = a.heads[c];
+            is = p.tiles > 0 && line_cut(total, c, BLOCKS) != p.start &&
+                 line_cut(total, c - 1, BLOCKS) <= p.start;
+            many = is && last_of(p) - c + 2 > kJoinFew;
         }
-        for (; q <= last; ++q) {
-            load(2 * q, f);
+        const uint32_t m[2] = {__ballot_sync(0xffffffffu, is && !many),
+                               __ballot_sync(0xffffffffu, many)};
+        __syncthreads();
+        if (lane < 2) warp_n[lane][warp] = __popc(m[lane]);
+        __syncthreads();
 #pragma unroll
-            for (int e = 0; e < V; ++e) v[e] += f[e];
-        }
-    } else {
-        // fewer tiles than blocks: a block has one or none
-        for (int q = c; q <= last; ++q) {
-            if (cut(q) == cut(q + 1)) continue;
-            load(2 * q, f);
+        for (int k = 0; k < 2; ++k) {
+            int at = n[k];
 #pragma unroll
-            for (int e = 0; e < V; ++e) v[e] += f[e];
+            for (int w = 0; w < kJoinWarps; ++w) {
+                if (w < warp) at += warp_n[k][w];
+                n[k] += warp_n[k][w];
+            }
+            if (is && many == (k == 1)) cuts[k][at + __popc(m[k] & ((1u << lane) - 1u))] = c;
         }
     }
-    const int r = i / a.dv;
-    store_out(static_cast<TOut*>(a.out) + (p.row + r) * a.out_stride +
-                  static_cast<int64_t>(p.h) * a.dv + (i - r * a.dv),
-              v, a.inv_n);
+    __syncthreads();
+    const int values = NQ * a.dv;
+    const int per_few = (values + kJoinThreads * V - 1) / (kJoinThreads * V);
+    const int per_many = (values + 32 * V - 1) / (32 * V);
+    for (int u = blockIdx.x; u < n[0] * per_few + n[1] * per_many; u += gridDim.x) {
+        const bool many = u >= n[0] * per_few;
+        const int x = many ? u - n[0] * per_few : u;
+        const int c = many ? cuts[1][x / per_many] : cuts[0][x / per_few];
+        const PartHead p = a.heads[c];
+        const int i = (many ? x % per_many * 32 + lane : x % per_few * kJoinThreads + tid) * V;
+        const bool live = i < p.rows * a.dv;
+        const int parts = last_of(p) - c + 2;
+        const int q0 = many ? parts * warp / kJoinWarps : 0;
+        const int q1 = many ? parts * (warp + 1) / kJoinWarps : parts;
+        float v[V] = {};
+        const float* src = a.parts + i;
+#pragma unroll 4
+        for (int q = q0; q < q1; ++q) {
+            const int b = c - 1 + q;
+            // (with fewer tiles than blocks some have none)
+            const bool has = live && (total >= BLOCKS ||
+                                      line_cut(total, b, BLOCKS) < line_cut(total, b + 1, BLOCKS));
+            // c - 1's part is its last item's, its only one's when it begins with this item
+            const int part = 2 * b + (q == 0 && line_cut(total, b, BLOCKS) != p.start ? 1 : 0);
+            const float* s = src + static_cast<int64_t>(part) * values;
+            if constexpr (V == 4) {
+                const float4 f = has ? *reinterpret_cast<const float4*>(s) : make_float4(0.f, 0.f, 0.f, 0.f);
+                v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+            } else {
+                v[0] += has ? *s : 0.f;
+            }
+        }
+        if (many) {
+            __syncthreads();                // the previous unit's sums have been read
+#pragma unroll
+            for (int e = 0; e < V; ++e) sums[warp][lane * V + e] = v[e];
+            __syncthreads();
+            if (warp == 0) {
+#pragma unroll
+                for (int w = 1; w < kJoinWarps; ++w)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) v[e] += sums[w][lane * V + e];
+            }
+        }
+        if (live && (!many || warp == 0)) {
+            const int r = i / a.dv;
+            store_out(static_cast<TOut*>(a.out) + (p.row + r) * a.out_stride +
+                          static_cast<int64_t>(p.h) * a.dv + (i - r * a.dv),
+                      v, a.inv_n);
+        }
+    }
 }
 
 // ------------------------------------------------------------------ the tree
@@ -327,6 +372,7 @@ struct alignas(16) TreeSmem {
     uint32_t seen[kMaxTree / 32][kMaxTree];     // [query / 32][key]: bit of the query
     int16_t depth[kMaxTree];
     int16_t parent[kMaxTree];
+    int deepest;                                // greatest depth
 };
 
 // Built by `nt` threads (index t), which `sync` holds together; a parent that
@@ -335,6 +381,7 @@ template <typename Sync>
 __device__ __forceinline__ void build_tree(const CachedArgs& a, const CachedSeq& s, TreeSmem& tree,
                                            int t, int nt, Sync sync) {
     sync();                                     // the previous tree is no longer read
+    if (t == 0) tree.deepest = 0;
     const int words = (s.n + 31) / 32;
     for (int m = t; m < s.n; m += nt) {
         const int p = a.parents[s.off + m];
@@ -351,6 +398,7 @@ __device__ __forceinline__ void build_tree(const CachedArgs& a, const CachedSeq&
             ++d;
         }
         tree.depth[m] = static_cast<int16_t>(d);
+        atomicMax(&tree.deepest, d);
     }
     sync();
 }

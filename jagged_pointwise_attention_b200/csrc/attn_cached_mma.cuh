@@ -163,8 +163,6 @@ attn_cached_mma_kernel(const __grid_constant__ CUtensorMap tmK,
     };
     seek();
     __syncwarp();
-#pragma unroll 1
-    for (int s = 0; s < ST; ++s) issue();
 
     // ---- the items
     int stage = 0;
@@ -182,15 +180,16 @@ attn_cached_mma_kernel(const __grid_constant__ CUtensorMap tmK,
         }
         const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(a.q) +
                                   (at.s.off + q0) * a.q_stride + static_cast<int64_t>(at.h) * D;
-        __syncthreads();        // the previous item's tables and sums have been read
-        if (use_time) {
-            if (tid < NQ) tqs[tid] = a.ts[at.s.off + q0 + min(tid, rows - 1)];
-            if (head_of != at.h && tid >= 64 && tid < 128)
-                tbs[tid - 64] = a.tb[static_cast<int64_t>(at.h) * a.NB + min(tid - 64, a.NB - 1)];
-            head_of = at.h;
-        }
+        // the item's own loads are on their way before the ring's first ones
+        const int64_t tq_mine = use_time && tid < NQ ? __ldg(a.ts + at.s.off + q0 + min(tid, rows - 1)) : 0;
+        const bool new_head = use_time && head_of != at.h && tid >= 64 && tid < 128;
+        const float tb_mine = new_head ? __ldg(a.tb + static_cast<int64_t>(at.h) * a.NB +
+                                               min(tid - 64, a.NB - 1))
+                                       : 0.f;
+        head_of = at.h;
         // Q^T fragments; queries behind the last are zeros
         uint32_t qf[kQRegs ? NT : 1][KS][2];
+        if (!kQRegs) __syncthreads();   // the previous item's sums have been read
         if (kQRegs) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -210,6 +209,13 @@ attn_cached_mma_kernel(const __grid_constant__ CUtensorMap tmK,
                 *reinterpret_cast<uint4*>(smem + S::kOffQ + r * S::kQPitch + 16 * c) = v;
             }
         }
+        if (first_item) {
+#pragma unroll 1
+            for (int s = 0; s < ST; ++s) issue();
+        }
+        __syncthreads();        // the previous item's tables and sums have been read
+        if (use_time && tid < NQ) tqs[tid] = tq_mine;
+        if (new_head) tbs[tid - 64] = tb_mine;
         int pq[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n)

@@ -64,12 +64,10 @@ hstu_status_t validate_cached(hstu_dtype_t dtype, const CachedArgs& c, int32_t p
 }
 
 // The join of parts, as a programmatic dependent of the attention launch.
-template <int NQ, int V, typename TOut>
-hstu_status_t launch_join(const CachedArgs& a, int blocks, cudaStream_t stream) {
+template <int NQ, int V, typename TOut, int BLOCKS>
+hstu_status_t launch_join(const CachedArgs& a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    constexpr int per = kJoinThreads * V;
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks - 1),
-                       static_cast<unsigned>((NQ * a.dv + per - 1) / per));
+    cfg.gridDim = dim3(kJoinBlocks);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -77,7 +75,7 @@ hstu_status_t launch_join(const CachedArgs& a, int blocks, cudaStream_t stream) 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_cached_join_kernel<NQ, V, TOut>, a, blocks);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_cached_join_kernel<NQ, V, TOut, BLOCKS>, a);
     return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }
 
@@ -88,7 +86,7 @@ hstu_status_t launch_cached_simt(const CachedArgs& a, cudaStream_t stream) {
     if (!ensure_smem(attn_cached_simt_kernel<DMAX, VEC>, smem, done)) return HSTU_ERR_CUDA;
     attn_cached_simt_kernel<DMAX, VEC><<<kSimtBlocks, kSimtThreads, smem, stream>>>(a);
     const hstu_status_t st = launch_status();
-    return st == HSTU_OK ? launch_join<kSimtRows, 1, float>(a, kSimtBlocks, stream) : st;
+    return st == HSTU_OK ? launch_join<kSimtRows, 1, float, kSimtBlocks>(a, stream) : st;
 }
 
 template <bool VEC>
@@ -143,7 +141,7 @@ hstu_status_t launch_cached_mma(const CachedArgs& a, const CUtensorMap& tk, cons
     attn_cached_mma_kernel<D, NT, false>
         <<<kMmaBlocks, S::kThreads, S::kAlloc, stream>>>(tk, tv, a, qtiles);
     const hstu_status_t st = launch_status();
-    return st == HSTU_OK ? launch_join<NQ, 4, __nv_bfloat16>(a, kMmaBlocks, stream) : st;
+    return st == HSTU_OK ? launch_join<NQ, 4, __nv_bfloat16, kMmaBlocks>(a, stream) : st;
 }
 
 template <int D, int NQ>
@@ -159,7 +157,7 @@ hstu_status_t launch_cached_tc(const CachedArgs& a, cudaStream_t stream) {
     if (!ensure_smem(attn_cached_tc_kernel<D, NQ>, S::kAlloc, done)) return HSTU_ERR_CUDA;
     attn_cached_tc_kernel<D, NQ><<<kMmaBlocks, kTcThreads, S::kAlloc, stream>>>(tq, tk, tv, a);
     const hstu_status_t st = launch_status();
-    return st == HSTU_OK ? launch_join<NQ, 4, __nv_bfloat16>(a, kMmaBlocks, stream) : st;
+    return st == HSTU_OK ? launch_join<NQ, 4, __nv_bfloat16, kMmaBlocks>(a, stream) : st;
 }
 
 // Rows of a query tile: up to 16 on warp products (32 for heads of 32, which
