@@ -85,6 +85,7 @@ struct CachedArgs {
     float inv_n;
     struct PartHead* heads;         // workspace: one a block
     float* parts;                   // then two parts a block
+    int part_rows;                  // of part_rows x dv floats each
 };
 
 // What block c found at the start of its part of the line: the item there.
@@ -260,7 +261,7 @@ __device__ __forceinline__ void store_out(__nv_bfloat16* dst, const float (&v)[4
 }
 
 // Parts: block c's first item at 2c, its last (when that is another) at 2c + 1,
-// NQ * dv floats each. An item is shared where a cut lies strictly behind its
+// part_rows * dv floats each. An item is shared where a cut lies strictly behind its
 // first tile; the first such cut stands for it. Every block of the join reads
 // all heads at once and lists the shared items, those of up to kJoinFew parts
 // and those of more, and takes every gridDim-th unit of work: of the former
@@ -272,7 +273,7 @@ constexpr int kJoinThreads = kJoinWarps * 32;
 constexpr int kJoinBlocks = 3 * 148;
 constexpr int kJoinFew = 6;
 
-template <int NQ, int V, typename TOut, int BLOCKS>
+template <int V, typename TOut, int BLOCKS>
 __global__ void __launch_bounds__(kJoinThreads) attn_cached_join_kernel(const CachedArgs a) {
     __shared__ int cuts[2][BLOCKS];             // few, many
     __shared__ int warp_n[2][kJoinWarps];
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_cached_join_kernel(const Ca
         }
     }
     __syncthreads();
-    const int values = NQ * a.dv;
+    const int values = a.part_rows * a.dv;
     const int per_few = (values + kJoinThreads * V - 1) / (kJoinThreads * V);
     const int per_many = (values + 32 * V - 1) / (32 * V);
     for (int u = blockIdx.x; u < n[0] * per_few + n[1] * per_many; u += gridDim.x) {
@@ -401,6 +402,26 @@ __device__ __forceinline__ void build_tree(const CachedArgs& a, const CachedSeq&
         atomicMax(&tree.deepest, d);
     }
     sync();
+}
+
+// The weight of one key for one query, alone, from global memory: for the rare
+// keys whose values are not finite while some query of their tile does not see
+// them. Kept out of line, like all that only they need.
+template <int D>
+__device__ __noinline__ float odd_weight(const CachedArgs& a, int h, int64_t qrow, int pq, int page,
+                                         int row, int pk) {
+    const int64_t hd = static_cast<int64_t>(h) * D;
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + qrow * a.q_stride + hd;
+    const __nv_bfloat16* k =
+        static_cast<const __nv_bfloat16*>(a.k) + page * a.k_page + row * a.k_tok + hd;
+    float s = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < D; ++c) s = fmaf(__bfloat162float(q[c]), __bfloat162float(k[c]), s);
+    if (a.pos) s += a.pos[static_cast<int64_t>(h) * a.P + min(pq - pk, a.P - 1)];
+    if (a.tsc)
+        s += a.tb[static_cast<int64_t>(h) * a.NB +
+                  time_bucket64(a.ts[qrow] - a.tsc[page * a.tsc_page + row], a.NB - 1)];
+    return silu_exp(s);
 }
 
 }  // namespace hstu

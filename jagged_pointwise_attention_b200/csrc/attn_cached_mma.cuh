@@ -48,18 +48,44 @@ struct CachedMmaSmem {
     static constexpr int kOffPage = kOffBar + kWarps * kStages * 8;
     static constexpr int kOffScratch = kOffPage + kWarps * kStages * 4;
     static constexpr int kOffTree = (kOffScratch + (kWarps + 8) * 8 + 15) / 16 * 16;
-    static constexpr int kOffAbort = kOffTree + static_cast<int>(sizeof(TreeSmem));
+    static constexpr int kOffOdd = kOffTree + static_cast<int>(sizeof(TreeSmem));
+    static constexpr int kOffAbort = kOffOdd + 8 * 4;
     static constexpr int kBytes = kOffAbort + 16;
     static constexpr int kAlloc = kBytes + 1024;
     static_assert(kAlloc <= 227 * 1024, "shared memory per block");
 };
+
+// What the keys of `odd` (counted from part0) add to columns c, c + 1 of new
+// token qi.
+template <int D>
+__device__ __noinline__ float2 odd_sum(const CachedArgs& a, const uint32_t* odd, const TreeSmem& tree,
+                                       int64_t off, int b, int h, int ctx, int part0, int qi, int c) {
+    float2 sum = make_float2(0.f, 0.f);
+    const bool chain = a.parents == nullptr;
+#pragma unroll 1
+    for (int o = 0; o < kMaxTree; ++o) {
+        if (!((odd[o >> 5] >> (o & 31)) & 1u)) continue;
+        const int key = part0 + o, m = key - ctx;
+        if (chain ? m > qi : !((tree.seen[qi >> 5][m] >> (qi & 31)) & 1u)) continue;
+        const int page = a.table[static_cast<int64_t>(b) * a.table_stride + (key >> a.shift)];
+        const int row = key & ((1 << a.shift) - 1);
+        const float p = odd_weight<D>(a, h, off + qi, ctx + (chain ? qi : tree.depth[qi]),
+                                      page, row, chain ? key : ctx + tree.depth[m]);
+        const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) + page * a.v_page +
+                                 row * a.v_tok + static_cast<int64_t>(h) * D + c;
+        sum.x = fmaf(p, __bfloat162float(v[0]), sum.x);
+        sum.y = fmaf(p, __bfloat162float(v[1]), sum.y);
+    }
+    return sum;
+}
 
 // WHOLE: block i takes item i whole (short sequences: no part, no join, no
 // search); otherwise an equal part of the line.
 template <int D, int NT, bool WHOLE>
 __global__ void __launch_bounds__(CachedMmaSmem<D, NT, WHOLE>::kThreads, WHOLE ? 3 : 1)
 attn_cached_mma_kernel(const __grid_constant__ CUtensorMap tmK,
-                       const __grid_constant__ CUtensorMap tmV, const CachedArgs a, int qtiles) {
+                       const __grid_constant__ CUtensorMap tmV,
+                       const __grid_constant__ CachedArgs a, int qtiles) {
     using S = CachedMmaSmem<D, NT, WHOLE>;
     using L = Line<kMmaKeys, S::kNQ>;
     constexpr int NQ = S::kNQ, ST = S::kStages, KS = D / 16;
@@ -79,6 +105,7 @@ attn_cached_mma_kernel(const __grid_constant__ CUtensorMap tmK,
     int* pages = reinterpret_cast<int*>(smem + S::kOffPage) + warp * ST;
     int64_t* scratch = reinterpret_cast<int64_t*>(smem + S::kOffScratch);
     TreeSmem& tree = *reinterpret_cast<TreeSmem*>(smem + S::kOffTree);
+    uint32_t* odd = reinterpret_cast<uint32_t*>(smem + S::kOffOdd);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kOffAbort);
     const bool use_pos = a.pos != nullptr, use_time = a.tsc != nullptr;
 
@@ -174,6 +201,8 @@ attn_cached_mma_kernel(const __grid_constant__ CUtensorMap tmK,
         const int take = static_cast<int>(min(left, static_cast<int64_t>(nt - at.j)));
         const int q0 = at.qt * NQ, rows = min(NQ, at.s.n - q0);
         const int len = at.s.ctx + min(at.s.n, q0 + NQ);
+        // keys from here on are seen by some queries and not by others
+        const int part0 = at.s.ctx + (a.parents != nullptr ? 0 : q0);
         if (a.parents != nullptr && tree_of != at.b) {
             build_tree(a, at.s, tree, tid, kMmaThreads, [] { __syncthreads(); });
             tree_of = at.b;
@@ -215,6 +244,7 @@ attn_cached_mma_kernel(const __grid_constant__ CUtensorMap tmK,
         }
         __syncthreads();        // the previous item's tables and sums have been read
         if (use_time && tid < NQ) tqs[tid] = tq_mine;
+        if (tid >= 32 && tid < 40) odd[tid - 32] = 0u;      // new keys to be added alone
         if (new_head) tbs[tid - 64] = tb_mine;
         int pq[NT][2];
 #pragma unroll
@@ -330,7 +360,6 @@ attn_cached_mma_kernel(const __grid_constant__ CUtensorMap tmK,
                                 tqs[8 * n + 2 * t + (e & 1)] - (e >> 1 ? tk1 : tk0), 63)];
                 }
             }
-            uint32_t seen = 0u;         // bit 4n + e: the query sees the key
             uint32_t pf[NT][2];
             float p[NT][4];
 #pragma unroll
@@ -349,20 +378,17 @@ attn_cached_mma_kernel(const __grid_constant__ CUtensorMap tmK,
                                               : m <= qi);
                     }
                     p[n][e] = see ? silu_exp(f) : 0.f;
-                    seen |= static_cast<uint32_t>(see) << (4 * n + e);
                 }
                 pf[n][0] = movm_t(pack_bf16x2(p[n][0], p[n][1]));
                 pf[n][1] = movm_t(pack_bf16x2(p[n][2], p[n][3]));
             }
             // O^T += V^T P^T. Rows of V that some query does not see are
             // multiplied by zero, so they have to be finite: rows behind the
-            // sequence are cleared, and rows of new tokens with values that
-            // are not finite are added one by one to the queries that see
-            // them and then cleared.
+            // sequence and rows of new tokens that are not finite are cleared,
+            // and the latter are added alone to the queries that see them.
             if (tail) {
                 const int nk = min(kMmaKeys, len - k0);
-                uint32_t live = (1u << nk) - 1u;
-                uint32_t odd = 0u;
+                uint32_t gone = 0xffffu & ~((1u << nk) - 1u);
                 const int r = lane & 15;
                 if (k0 + r >= at.s.ctx && r < nk) {
                     bool bad = false;
@@ -378,43 +404,18 @@ attn_cached_mma_kernel(const __grid_constant__ CUtensorMap tmK,
                             bad = bad || (w[i] & 0x7f80u) == 0x7f80u ||
                                   (w[i] & 0x7f800000u) == 0x7f800000u;
                     }
-                    if (bad) odd = 1u << r;
-                }
-                odd = __reduce_or_sync(0xffffffffu, odd);
-                live &= ~odd;
-                while (odd) {
-                    const int kr = __ffs(odd) - 1;
-                    odd &= odd - 1u;
-                    const int src = (kr & 7) * 4 + t;       // the lane with this key's row
-                    const uint32_t sees = __shfl_sync(0xffffffffu, seen, src) >> (2 * (kr >> 3));
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const float lo0 = __shfl_sync(0xffffffffu, p[n][0], src);
-                        const float lo1 = __shfl_sync(0xffffffffu, p[n][1], src);
-                        const float hi0 = __shfl_sync(0xffffffffu, p[n][2], src);
-                        const float hi1 = __shfl_sync(0xffffffffu, p[n][3], src);
-                        const float w0 = kr < 8 ? lo0 : hi0, w1 = kr < 8 ? lo1 : hi1;
-#pragma unroll
-                        for (int m = 0; m < KS; ++m)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int d = 16 * m + g + 8 * (e >> 1), c = d >> 3;
-                                const int cc = D >= 64 ? ((c & 7) ^ (kr & 7)) : (c ^ ((kr >> 1) & 3));
-                                const __nv_bfloat16 v = *reinterpret_cast<const __nv_bfloat16*>(
-                                    ring + stage * S::kStageBytes + S::kHalfBytes +
-                                    (c >> 3) * S::kBoxBytes + kr * S::kRowBytes + (cc << 4) +
-                                    (d & 7) * 2);
-                                if ((sees >> (4 * n + (e & 1))) & 1u)
-                                    acc[m][n][e] = fmaf((e & 1) ? w1 : w0, __bfloat162float(v),
-                                                        acc[m][n][e]);
-                            }
+                    // (a key that a chain's whole tile sees counts as it is)
+                    if (bad && k0 + r >= part0) {
+                        gone |= 1u << r;
+                        atomicOr(&odd[(k0 + r - part0) >> 5], 1u << ((k0 + r - part0) & 31));
                     }
                 }
-                __syncwarp();
-                if (live != 0xffffu) {
+                gone = __reduce_or_sync(0xffffffffu, gone);
+                if (gone) {
+#pragma unroll 1
                     for (int i = lane; i < S::kHalfBytes / 16; i += 32) {
                         const int r = i * 16 / S::kRowBytes % kMmaKeys;
-                        if (!((live >> r) & 1u))
+                        if ((gone >> r) & 1u)
                             *reinterpret_cast<uint4*>(ring + stage * S::kStageBytes + S::kHalfBytes +
                                                       i * 16) = make_uint4(0u, 0u, 0u, 0u);
                     }
@@ -466,13 +467,21 @@ attn_cached_mma_kernel(const __grid_constant__ CUtensorMap tmK,
         }
         __syncthreads();
         const bool whole = WHOLE || take == nt;
-        float* part = a.parts + (2 * static_cast<int64_t>(blockIdx.x) + (first_item ? 0 : 1)) * NQ * D;
+        uint32_t any_odd = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) any_odd |= odd[i];
+        float* part = a.parts + (2 * static_cast<int64_t>(blockIdx.x) + (first_item ? 0 : 1)) * a.part_rows * D;
         for (int i = tid; i < rows * (D / 2); i += kMmaThreads) {
             const int r = i / (D / 2), c = 2 * (i % (D / 2));
             float2 v = make_float2(0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < S::kCopies; ++w) {
                 const float2 u = *reinterpret_cast<const float2*>(red + (w * NQ + r) * S::kPitch + c);
+                v.x += u.x;
+                v.y += u.y;
+            }
+            if (any_odd) {
+                const float2 u = odd_sum<D>(a, odd, tree, at.s.off, at.b, at.h, at.s.ctx, part0, q0 + r, c);
                 v.x += u.x;
                 v.y += u.y;
             }

@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_cached_simt_kernel(const Ca
         if (grp == 0 && col < a.dv) {
             const bool whole = take == nt;
             float* part = a.parts + (2 * static_cast<int64_t>(blockIdx.x) + (first_item ? 0 : 1)) *
-                                        kSimtRows * a.dv;
+                                        a.part_rows * a.dv;
 #pragma unroll
             for (int i = 0; i < kSimtRows; ++i) {
                 if (i >= rows) break;

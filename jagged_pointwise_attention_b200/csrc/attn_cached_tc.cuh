@@ -153,7 +153,6 @@ __device__ __noinline__ void add_odd_keys(const CachedArgs& a, const TcTables<NQ
         const int m = first_new + o, key = ctx + m;
         const int pg = a.table[static_cast<int64_t>(b) * a.table_stride + (key >> a.shift)];
         const int row = key & ((1 << a.shift) - 1);
-        const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k) + pg * a.k_page + row * a.k_tok + hd;
         const float v = __bfloat162float(
             static_cast<const __nv_bfloat16*>(a.v)[pg * a.v_page + row * a.v_tok + hd + d]);
         const int pk = chain ? key : ctx + tree.depth[m];
@@ -163,19 +162,8 @@ __device__ __noinline__ void add_odd_keys(const CachedArgs& a, const TcTables<NQ
             const bool see =
                 c < rows && (chain ? m <= qi : ((tree.seen[c >> 5][m] >> (c & 31)) & 1u) != 0u);
             float p = 0.f;
-            if (see) {
-                const __nv_bfloat16* q =
-                    static_cast<const __nv_bfloat16*>(a.q) + (row0 + c) * a.q_stride + hd;
-                float s = 0.f;
-#pragma unroll 1
-                for (int x = 0; x < D; ++x)
-                    s = fmaf(__bfloat162float(q[x]), __bfloat162float(k[x]), s);
-                if (a.pos)
-                    s += a.pos[static_cast<int64_t>(h) * a.P +
-                               min(ctx + first_new + T.qo[c] / 4 - pk, a.P - 1)];
-                if (a.tsc) s += T.tb[time_bucket64(T.tq[c] - a.tsc[pg * a.tsc_page + row], 63)];
-                p = silu_exp(s);
-            }
+            if (see)
+                p = odd_weight<D>(a, h, row0 + c, ctx + first_new + T.qo[c] / 4, pg, row, pk);
             const uint32_t sees = __ballot_sync(0xffffffffu, see);
 #pragma unroll 1
             for (int e = 0; e < 32 && c0 + e < rows; ++e) {
@@ -819,7 +807,8 @@ attn_cached_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
             for (int o = 0; o < 8; ++o) any_odd |= T.odd[o];
             // (with odd keys the rows go through the block's part, whole or not)
             const bool whole = I.whole && !any_odd;
-            float* part = a.parts + (2 * static_cast<int64_t>(blockIdx.x) + (it == 0 ? 0 : 1)) * NQ * D + d;
+            float* part = a.parts + (2 * static_cast<int64_t>(blockIdx.x) + (it == 0 ? 0 : 1)) * a.part_rows * D +
+                          d;
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + I.row0 * a.out_stride +
                                  static_cast<int64_t>(I.h) * D + (d & ~1);
             const int odd_lane = lane & 1;

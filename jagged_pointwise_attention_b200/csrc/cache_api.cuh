@@ -64,7 +64,7 @@ hstu_status_t validate_cached(hstu_dtype_t dtype, const CachedArgs& c, int32_t p
 }
 
 // The join of parts, as a programmatic dependent of the attention launch.
-template <int NQ, int V, typename TOut, int BLOCKS>
+template <int V, typename TOut, int BLOCKS>
 hstu_status_t launch_join(const CachedArgs& a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kJoinBlocks);
@@ -75,7 +75,7 @@ hstu_status_t launch_join(const CachedArgs& a, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_cached_join_kernel<NQ, V, TOut, BLOCKS>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_cached_join_kernel<V, TOut, BLOCKS>, a);
     return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }
 
@@ -86,7 +86,7 @@ hstu_status_t launch_cached_simt(const CachedArgs& a, cudaStream_t stream) {
     if (!ensure_smem(attn_cached_simt_kernel<DMAX, VEC>, smem, done)) return HSTU_ERR_CUDA;
     attn_cached_simt_kernel<DMAX, VEC><<<kSimtBlocks, kSimtThreads, smem, stream>>>(a);
     const hstu_status_t st = launch_status();
-    return st == HSTU_OK ? launch_join<kSimtRows, 1, float, kSimtBlocks>(a, stream) : st;
+    return st == HSTU_OK ? launch_join<1, float, kSimtBlocks>(a, stream) : st;
 }
 
 template <bool VEC>
@@ -117,31 +117,27 @@ bool make_tmap_cache(CUtensorMap* tm, const void* base, const CachedArgs& a, int
 }
 
 constexpr int kMmaBlocks = 148;
-// Sequences up to this length are taken whole by a block each: at most sixteen
-// groups a warp, about what the search of the line and the join cost.
-constexpr int kWholeLen = 1024;
+// Sequences are taken whole, a block each, where they are short enough: up to
+// 256 tokens always, up to 1024 when the items fill the device twice. (Heads of
+// 128, one new token, four heads: 128 sequences of 256 take 22 us whole and 33
+// along the line, of 1024 50 and 52; one sequence of 1000 26 and 15.)
+constexpr int kWholeLen = 256, kWholeLenFull = 1024;
 
-template <int D, int NT>
-hstu_status_t launch_cached_mma(const CachedArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
-                                cudaStream_t stream) {
-    constexpr int NQ = 8 * NT;
-    const int qtiles = (a.max_new + NQ - 1) / NQ;
-    const int64_t items = static_cast<int64_t>(a.B) * qtiles * a.H;
-    if (a.max_seqlen <= kWholeLen && items <= 0x7fffffff) {
-        using S = CachedMmaSmem<D, NT, true>;
-        static int done[kMaxDevices] = {0};
-        if (!ensure_smem(attn_cached_mma_kernel<D, NT, true>, S::kAlloc, done)) return HSTU_ERR_CUDA;
-        attn_cached_mma_kernel<D, NT, true>
-            <<<static_cast<unsigned>(items), S::kThreads, S::kAlloc, stream>>>(tk, tv, a, qtiles);
-        return launch_status();
-    }
-    using S = CachedMmaSmem<D, NT, false>;
+template <int D, int NT, bool WHOLE>
+hstu_status_t launch_cached_mma(const CachedArgs& a, int64_t items, cudaStream_t stream) {
+    using S = CachedMmaSmem<D, NT, WHOLE>;
     static int done[kMaxDevices] = {0};
-    if (!ensure_smem(attn_cached_mma_kernel<D, NT, false>, S::kAlloc, done)) return HSTU_ERR_CUDA;
-    attn_cached_mma_kernel<D, NT, false>
-        <<<kMmaBlocks, S::kThreads, S::kAlloc, stream>>>(tk, tv, a, qtiles);
+    CUtensorMap tk, tv;
+    if (!make_tmap_cache(&tk, a.k, a, a.k_page, a.k_tok, kMmaKeys) ||
+        !make_tmap_cache(&tv, a.v, a, a.v_page, a.v_tok, kMmaKeys) ||
+        !ensure_smem(attn_cached_mma_kernel<D, NT, WHOLE>, S::kAlloc, done))
+        return HSTU_ERR_CUDA;
+    attn_cached_mma_kernel<D, NT, WHOLE>
+        <<<WHOLE ? static_cast<unsigned>(items) : kMmaBlocks, S::kThreads, S::kAlloc, stream>>>(
+            tk, tv, a, (a.max_new + 8 * NT - 1) / (8 * NT));
     const hstu_status_t st = launch_status();
-    return st == HSTU_OK ? launch_join<NQ, 4, __nv_bfloat16, kMmaBlocks>(a, stream) : st;
+    if (WHOLE || st != HSTU_OK) return st;
+    return launch_join<4, __nv_bfloat16, kMmaBlocks>(a, stream);
 }
 
 template <int D, int NQ>
@@ -157,32 +153,45 @@ hstu_status_t launch_cached_tc(const CachedArgs& a, cudaStream_t stream) {
     if (!ensure_smem(attn_cached_tc_kernel<D, NQ>, S::kAlloc, done)) return HSTU_ERR_CUDA;
     attn_cached_tc_kernel<D, NQ><<<kMmaBlocks, kTcThreads, S::kAlloc, stream>>>(tq, tk, tv, a);
     const hstu_status_t st = launch_status();
-    return st == HSTU_OK ? launch_join<NQ, 4, __nv_bfloat16, kMmaBlocks>(a, stream) : st;
+    return st == HSTU_OK ? launch_join<4, __nv_bfloat16, kMmaBlocks>(a, stream) : st;
 }
 
-// Rows of a query tile: up to 16 on warp products (32 for heads of 32, which
-// the tcgen05 kernel does not take), then 64 and 128.
-int cached_rows(int32_t max_new, int32_t d) {
-    if (max_new <= 8) return 8;
-    if (max_new <= 16) return 16;
-    return d == 32 ? 32 : max_new <= 64 ? 64 : 128;
+// Rows of a part: the most that an item of the kernels below can have.
+int cached_part_rows(hstu_dtype_t dtype, int32_t max_new, int32_t d) {
+    if (dtype == HSTU_DTYPE_F32) return kSimtRows;
+    const int most = d == 32 ? 32 : 128;
+    return max_new >= most ? most : (max_new + 7) / 8 * 8;
 }
 
+// Items of query tiles of `rows` where every sequence may be taken whole, else 0.
+int64_t cached_whole_items(const CachedArgs& a, int rows) {
+    const int64_t items = static_cast<int64_t>(a.B) * ((a.max_new + rows - 1) / rows) * a.H;
+    const bool whole = a.max_seqlen <= kWholeLen ||
+                       (a.max_seqlen <= kWholeLenFull && items >= 2 * kMmaBlocks);
+    return whole && items <= 0x7fffffff ? items : 0;
+}
+
+// Heads of 64 and 128: the tcgen05 kernel, but for up to eight new tokens over
+// short sequences.
 template <int D>
 hstu_status_t run_cached_bf16(const CachedArgs& a, cudaStream_t stream) {
-    const int rows = cached_rows(a.max_new, D);
-    if constexpr (D != 32) {
-        if (rows == 64) return launch_cached_tc<D, 64>(a, stream);
-        if (rows == 128) return launch_cached_tc<D, 128>(a, stream);
-    }
-    CUtensorMap tk, tv;
-    if (!make_tmap_cache(&tk, a.k, a, a.k_page, a.k_tok, kMmaKeys) ||
-        !make_tmap_cache(&tv, a.v, a, a.v_page, a.v_tok, kMmaKeys))
-        return HSTU_ERR_CUDA;
-    if constexpr (D == 32)
-        if (rows == 32) return launch_cached_mma<D, 4>(a, tk, tv, stream);
-    return rows == 8 ? launch_cached_mma<D, 1>(a, tk, tv, stream)
-                     : launch_cached_mma<D, 2>(a, tk, tv, stream);
+    const int64_t items = cached_whole_items(a, 8);
+    if (a.max_new <= 8 && items) return launch_cached_mma<D, 1, true>(a, items, stream);
+    return a.max_new <= 64 ? launch_cached_tc<D, 64>(a, stream) : launch_cached_tc<D, 128>(a, stream);
+}
+
+template <int NT>
+hstu_status_t run_cached_bf16_d32(const CachedArgs& a, cudaStream_t stream) {
+    const int64_t items = cached_whole_items(a, 8 * NT);
+    return items ? launch_cached_mma<32, NT, true>(a, items, stream)
+                 : launch_cached_mma<32, NT, false>(a, 0, stream);
+}
+
+template <>
+hstu_status_t run_cached_bf16<32>(const CachedArgs& a, cudaStream_t stream) {
+    return a.max_new <= 8    ? run_cached_bf16_d32<1>(a, stream)
+           : a.max_new <= 16 ? run_cached_bf16_d32<2>(a, stream)
+                             : run_cached_bf16_d32<4>(a, stream);
 }
 
 template <int MT, int NT, int G>
@@ -302,8 +311,8 @@ size_t hstu_attn_cached_workspace_bytes(hstu_dtype_t dtype, int32_t max_new, int
         d_v > 128)
         return 0;
     const size_t blocks = dtype == HSTU_DTYPE_F32 ? kSimtBlocks : kMmaBlocks;
-    const size_t rows = dtype == HSTU_DTYPE_F32 ? kSimtRows : cached_rows(max_new, d_v);
-    return blocks * (sizeof(PartHead) + 2 * rows * d_v * 4);
+    return blocks * (sizeof(PartHead) +
+                     static_cast<size_t>(2) * cached_part_rows(dtype, max_new, d_v) * d_v * 4);
 }
 
 hstu_status_t hstu_attn_cached_fwd(hstu_dtype_t dtype, const void* q, int64_t q_tok_stride,
@@ -358,6 +367,7 @@ hstu_status_t hstu_attn_cached_fwd(hstu_dtype_t dtype, const void* q, int64_t q_
     a.inv_n = 1.0f / static_cast<float>(max_seqlen);
     a.heads = static_cast<PartHead*>(workspace);
     a.parts = reinterpret_cast<float*>(a.heads + (dtype == HSTU_DTYPE_F32 ? kSimtBlocks : kMmaBlocks));
+    a.part_rows = cached_part_rows(dtype, max_new, d_v);
     const hstu_status_t st =
         validate_cached(dtype, a, page_size, workspace, workspace_bytes,
                         hstu_attn_cached_workspace_bytes(dtype, max_new, d_v));
