@@ -528,6 +528,36 @@ hstu_status_t hstu_linear_w4_fwd(const void* x, int64_t ldx, int64_t M, int32_t 
                                  const void* residual, int64_t ldr, void* y, int64_t ldy,
                                  void* stream);
 
+/* Workspace bytes of hstu_layer_step_fwd. */
+size_t hstu_layer_step_workspace_bytes(int64_t total_new, int32_t D, int32_t H, int32_t d,
+                                       int32_t max_new);
+
+/* hstu_layer_fwd for the new tokens of a serving step: x and out are their
+ * [total_new, D] rows, K, V and the timestamps go to the cache at `slots`
+ * (hstu_cache_plan; ts_cache and timestamps: both or neither), and the
+ * attention is hstu_attn_cached_fwd, so chains, trees and candidates are all
+ * possible. w4_group 0: W1 and W2 are bf16 as in hstu_layer_fwd, s1 and s2 are
+ * not read. w4_group 32, 64 or 128: W1 and W2 are codes [4 H d, D/2] and
+ * [D, H d/2] with scales s1 [4 H d, D/group] and s2 [D, H d/group] as
+ * hstu_quant_groups_w4 writes them, rows without gaps. Sizes as hstu_layer_fwd;
+ * cache, batch and the rest as hstu_cache_append and hstu_attn_cached_fwd. */
+hstu_status_t hstu_layer_step_fwd(const void* x, int64_t total_new, int32_t D, const void* W1,
+                                  const void* s1, const float* b1, const void* W2, const void* s2,
+                                  const float* b2, int32_t w4_group, const float* ln_gamma,
+                                  const float* ln_beta, float ln_eps, int32_t input_norm,
+                                  const float* in_gamma, const float* in_beta, void* k_cache,
+                                  int64_t k_page_stride, int64_t k_tok_stride, void* v_cache,
+                                  int64_t v_page_stride, int64_t v_tok_stride, int64_t* ts_cache,
+                                  int64_t ts_page_stride, int32_t num_pages, int32_t page_size,
+                                  const int32_t* block_table, int64_t table_stride,
+                                  int32_t max_pages, const int32_t* ctx_lens,
+                                  const int64_t* new_offsets, int32_t B, const int64_t* slots,
+                                  int32_t max_new, int32_t H, int32_t d, const int64_t* timestamps,
+                                  const int32_t* parents, const float* pos_bias, int32_t num_pos,
+                                  const float* time_bias, int32_t num_time_buckets,
+                                  int32_t max_seqlen, void* out, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -30,6 +30,7 @@ __all__ = [
     "hstu_layer_fp8_workspace_bytes", "hstu_layer_fp8_fwd",
     "hstu_cache_plan", "hstu_cache_append", "hstu_attn_cached_fwd",
     "hstu_attn_cached_workspace_bytes", "hstu_quant_groups_w4", "hstu_linear_w4_fwd",
+    "hstu_layer_step_fwd", "hstu_layer_step_workspace_bytes",
     "hstu_device_status", "HstuError", "library_path",
 ]
 
@@ -519,3 +520,93 @@ def hstu_linear_w4_fwd(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tenso
     or "residual" (adds `residual`). x [M, K] bf16, returns bf16 [M, N]."""
     return _native.serving().linear_w4(x, codes, scales, bias, _EPILOGUES[epilogue], residual, out,
                                        _raw(stream))
+
+
+def hstu_layer_step_workspace_bytes(total_new: int, D: int, H: int, d: int, max_new: int) -> int:
+    return int(_lib().hstu_layer_step_workspace_bytes(total_new, D, H, d, max_new))
+
+
+def hstu_layer_step_fwd(x: torch.Tensor, W1, W2, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                        ts_cache: Optional[torch.Tensor], block_table: torch.Tensor,
+                        ctx_lens: torch.Tensor, new_offsets: torch.Tensor, slots: torch.Tensor,
+                        timestamps: Optional[torch.Tensor], parents: Optional[torch.Tensor],
+                        pos_bias: Optional[torch.Tensor], time_bias: Optional[torch.Tensor],
+                        max_seqlen: int, max_new: int, b1=None, b2=None, ln_gamma=None,
+                        ln_beta=None, ln_eps: float = 1e-5, out: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None,
+                        input_norm: bool = False, in_gamma=None, in_beta=None) -> torch.Tensor:
+    """One HSTU layer for the new tokens of a serving step: hstu_layer_fwd on
+    their rows x [T, D], whose keys, values and timestamps go to the cache at
+    `slots` (hstu_cache_plan) and whose attention is hstu_attn_cached_fwd. W1
+    and W2 are bf16 [4Hd, D] and [D, Hd], or each a (codes, scales) pair from
+    hstu_quant_groups_w4 with one group size. Arguments as in those calls."""
+    w4 = isinstance(W1, (tuple, list))
+    if isinstance(W2, (tuple, list)) != w4:
+        raise TypeError("W1 and W2 are both bf16 or both (codes, scales)")
+    (c1, s1), (c2, s2) = (W1, W2) if w4 else ((W1, None), (W2, None))
+    dev = torch.cuda.current_device()
+    for t in (x, c1, s1, c2, s2, k_cache, v_cache, ts_cache, block_table, ctx_lens, new_offsets,
+              slots, timestamps, parents, pos_bias, time_bias, b1, b2, ln_gamma, ln_beta, in_gamma,
+              in_beta, out, workspace):
+        if t is not None and t.get_device() != dev:
+            raise ValueError("all tensors must be on the current CUDA device")
+    T, D = x.shape
+    n, page, H, d = k_cache.shape
+    F, B = H * d, new_offsets.numel() - 1
+    group = 0
+    if w4:
+        if s1.dim() != 2 or s1.shape[1] < 1 or D % s1.shape[1]:
+            raise ValueError("W1's scales must be [4Hd, D / group]")
+        group = D // s1.shape[1]
+    want = [(x, torch.bfloat16, (T, D)), (out, torch.bfloat16, (T, D)),
+            (block_table, torch.int32, (B, block_table.shape[-1])), (ctx_lens, torch.int32, (B,)),
+            (new_offsets, torch.int64, (B + 1,)), (slots, torch.int64, (T,)),
+            (timestamps, torch.int64, (T,)), (parents, torch.int32, (T,)),
+            (ts_cache, torch.int64, (n, page)),
+            (b1, torch.float32, (4 * F,)), (b2, torch.float32, (D,)),
+            (ln_gamma, torch.float32, (F,)), (ln_beta, torch.float32, (F,)),
+            (in_gamma, torch.float32, (D,)), (in_beta, torch.float32, (D,))]
+    if w4:
+        want += [(c1, torch.uint8, (4 * F, D // 2)), (s1, torch.bfloat16, (4 * F, D // group)),
+                 (c2, torch.uint8, (D, F // 2)), (s2, torch.bfloat16, (D, F // group))]
+    else:
+        want += [(c1, torch.bfloat16, (4 * F, D)), (c2, torch.bfloat16, (D, F))]
+    for t, dtype, shape in want:
+        if t is not None and t.dtype != dtype:
+            raise TypeError("expected %s, got %s" % (dtype, t.dtype))
+        if t is not None and (tuple(t.shape) != shape or not t.is_contiguous()):
+            raise ValueError("expected a contiguous %s, got %s" % (list(shape), list(t.shape)))
+    for t in (k_cache, v_cache):
+        if t.dtype != torch.bfloat16:
+            raise TypeError("the caches must be bfloat16")
+        if tuple(t.shape) != (n, page, H, d) or t.stride(3) != 1 or (H > 1 and t.stride(2) != d):
+            raise ValueError("the caches must be [num_pages, page_size, H, d], tokens contiguous")
+    for t in (pos_bias, time_bias):
+        if t is not None and (t.dtype != torch.float32 or t.dim() != 2 or t.shape[0] != H
+                              or not t.is_contiguous()):
+            raise ValueError("bias tables must be contiguous float32 [H, entries]")
+    own = []
+    if out is None:
+        out = torch.empty_like(x)
+        own.append(out)
+    if workspace is None:
+        workspace = _workspace(hstu_layer_step_workspace_bytes(T, D, H, d, max_new), x.device)
+        own.append(workspace)
+    strides = [s for t in (k_cache, v_cache)
+               for s in (t.stride(0) if n > 1 else page * t.stride(1), t.stride(1))]
+    _native.check("hstu_layer_step_fwd", _lib().hstu_layer_step_fwd(
+        _ptr(x), T, D, _ptr(c1), _ptr(s1), _ptr(b1), _ptr(c2), _ptr(s2), _ptr(b2), group,
+        _ptr(ln_gamma), _ptr(ln_beta), float(ln_eps), 1 if input_norm else 0, _ptr(in_gamma),
+        _ptr(in_beta), _ptr(k_cache), strides[0], strides[1], _ptr(v_cache), strides[2], strides[3],
+        _ptr(ts_cache), page, n, page, _ptr(block_table), block_table.shape[1],
+        block_table.shape[1], _ptr(ctx_lens), _ptr(new_offsets), B, _ptr(slots), int(max_new), H, d,
+        _ptr(timestamps), _ptr(parents), _ptr(pos_bias),
+        0 if pos_bias is None else pos_bias.shape[1], _ptr(time_bias),
+        0 if time_bias is None else time_bias.shape[1], int(max_seqlen), _ptr(out),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+    if stream is not None:
+        # allocated here and used on a stream that may not be the current one
+        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+        for t in own:
+            t.record_stream(s)
+    return out

@@ -73,6 +73,13 @@ SIGNATURES = {
                                             c_i32, c_p, c_p, c_i32, c_i64, c_i32, c_i32, c_i32,
                                             c_i32, c_p, c_p, c_p, c_i32, c_p, c_i32, c_i32, c_p,
                                             c_i64, c_p, c_sz, c_p]),
+    "hstu_layer_step_workspace_bytes": (c_sz, [c_i64, c_i32, c_i32, c_i32, c_i32]),
+    "hstu_layer_step_fwd": (ctypes.c_int, [c_p, c_i64, c_i32, c_p, c_p, c_p, c_p, c_p, c_p, c_i32,
+                                           c_p, c_p, c_f32, c_i32, c_p, c_p, c_p, c_i64, c_i64,
+                                           c_p, c_i64, c_i64, c_p, c_i64, c_i32, c_i32, c_p, c_i64,
+                                           c_i32, c_p, c_p, c_i32, c_p, c_i32, c_i32, c_i32, c_p,
+                                           c_p, c_p, c_i32, c_p, c_i32, c_i32, c_p, c_p, c_sz,
+                                           c_p]),
     "hstu_quant_groups_w4": (ctypes.c_int, [c_p, c_i64, c_i64, c_i32, c_i32, c_p, c_i64, c_p,
                                             c_i64, c_p]),
     "hstu_linear_w4_fwd": (ctypes.c_int, [c_p, c_i64, c_i64, c_i32, c_p, c_i64, c_p, c_i64, c_i32,

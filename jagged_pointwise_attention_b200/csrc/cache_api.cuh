@@ -231,6 +231,27 @@ hstu_status_t run_linear_w4(const LinearW4Args& a, cudaStream_t stream) {
     return launch_linear_w4_g<1, 8>(a, warps, stream);
 }
 
+// workspace of a layer step: [LayerNorm(x)][U|V|Q|K][attention][gated rows][attention's own]
+struct LayerStepWs {
+    size_t xn, uvqk, attn, y, own, total;
+};
+
+LayerStepWs layer_step_ws(int64_t T, int32_t D, int32_t H, int32_t d, int32_t max_new) {
+    const size_t t = static_cast<size_t>(T), F = static_cast<size_t>(H) * d;
+    LayerStepWs w;
+    w.xn = 0;
+    w.uvqk = round_up(w.xn + t * D * 2, 256);
+    w.attn = round_up(w.uvqk + t * 4 * F * 2, 256);
+    w.y = round_up(w.attn + t * F * 2, 256);
+    w.own = round_up(w.y + t * F * 2, 256);
+    w.total = w.own + hstu_attn_cached_workspace_bytes(HSTU_DTYPE_BF16, max_new, d);
+    return w;
+}
+
+bool layer_step_sizes_ok(int64_t T, int32_t D, int32_t H, int32_t d, int32_t max_new) {
+    return T >= 0 && T <= 0x7fffffff && D >= 1 && H >= 1 && d >= 1 && max_new >= 1;
+}
+
 }  // namespace
 
 extern "C" {
@@ -432,6 +453,81 @@ hstu_status_t hstu_linear_w4_fwd(const void* x, int64_t ldx, int64_t M, int32_t 
                    static_cast<const __nv_bfloat16*>(residual), ldr,
                    static_cast<__nv_bfloat16*>(y), ldy, static_cast<int>(epilogue)};
     return run_linear_w4(a, as_stream(stream));
+}
+
+size_t hstu_layer_step_workspace_bytes(int64_t total_new, int32_t D, int32_t H, int32_t d,
+                                       int32_t max_new) {
+    if (!layer_step_sizes_ok(total_new, D, H, d, max_new) || (d != 64 && d != 128)) return 0;
+    return layer_step_ws(total_new, D, H, d, max_new).total;
+}
+
+hstu_status_t hstu_layer_step_fwd(const void* x, int64_t total_new, int32_t D, const void* W1,
+                                  const void* s1, const float* b1, const void* W2, const void* s2,
+                                  const float* b2, int32_t w4_group, const float* ln_gamma,
+                                  const float* ln_beta, float ln_eps, int32_t input_norm,
+                                  const float* in_gamma, const float* in_beta, void* k_cache,
+                                  int64_t k_page_stride, int64_t k_tok_stride, void* v_cache,
+                                  int64_t v_page_stride, int64_t v_tok_stride, int64_t* ts_cache,
+                                  int64_t ts_page_stride, int32_t num_pages, int32_t page_size,
+                                  const int32_t* block_table, int64_t table_stride,
+                                  int32_t max_pages, const int32_t* ctx_lens,
+                                  const int64_t* new_offsets, int32_t B, const int64_t* slots,
+                                  int32_t max_new, int32_t H, int32_t d, const int64_t* timestamps,
+                                  const int32_t* parents, const float* pos_bias, int32_t num_pos,
+                                  const float* time_bias, int32_t num_time_buckets,
+                                  int32_t max_seqlen, void* out, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+    const int64_t T = total_new;
+    if (!layer_step_sizes_ok(T, D, H, d, max_new) || B < 0) return HSTU_ERR_INVALID_ARG;
+    if (H > 65535 || (d != 64 && d != 128)) return HSTU_ERR_UNSUPPORTED;
+    const int32_t F = H * d;
+    if (D % 128 || F % 256 || F > 2048) return HSTU_ERR_UNSUPPORTED;
+    if (input_norm && (D % 256 || D > 2048)) return HSTU_ERR_UNSUPPORTED;
+    if (w4_group && w4_group != 32 && w4_group != 64 && w4_group != 128) return HSTU_ERR_UNSUPPORTED;
+    if ((timestamps == nullptr) != (ts_cache == nullptr)) return HSTU_ERR_INVALID_ARG;
+    if (T == 0 || B == 0) return HSTU_OK;
+    if (!x || !W1 || !W2 || !out || !slots || !workspace || (w4_group && (!s1 || !s2)))
+        return HSTU_ERR_INVALID_ARG;
+    const LayerStepWs w = layer_step_ws(T, D, H, d, max_new);
+    if (workspace_bytes < w.total || !aligned16(workspace)) return HSTU_ERR_INVALID_ARG;
+    cudaStream_t s = as_stream(stream);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    __nv_bfloat16* uvqk = reinterpret_cast<__nv_bfloat16*>(ws + w.uvqk);
+    __nv_bfloat16* attn = reinterpret_cast<__nv_bfloat16*>(ws + w.attn);
+    __nv_bfloat16* ygate = reinterpret_cast<__nv_bfloat16*>(ws + w.y);
+    auto project = [&](const void* a, int32_t K, const void* W, const void* sc, int32_t N,
+                       const float* b, hstu_epilogue_t epi, const void* r, void* y) {
+        if (w4_group)
+            return hstu_linear_w4_fwd(a, K, T, K, W, K / 2, sc, K / w4_group, w4_group, N, b, epi, r, N,
+                                      y, N, stream);
+        return run_linear(a, K, T, K, W, K, N, b, epi, r, N, y, N, s);
+    };
+    // 1. [LayerNorm(x) ->] f1 with the SiLU epilogue
+    const void* xin = x;
+    hstu_status_t st = HSTU_OK;
+    if (input_norm) {
+        xin = ws + w.xn;
+        st = run_ln_gate_any(false, false, x, D, nullptr, 0, T, D, in_gamma, in_beta, ln_eps, ws + w.xn,
+                             D, nullptr, 0, nullptr, s);
+        if (st != HSTU_OK) return st;
+    }
+    st = project(xin, D, W1, s1, 4 * F, b1, HSTU_EPI_SILU, nullptr, uvqk);
+    if (st != HSTU_OK) return st;
+    // 2. the new keys and values into the cache, then the attention over it
+    st = hstu_cache_append(HSTU_DTYPE_BF16, uvqk + 3 * F, 4 * F, uvqk + F, 4 * F, timestamps, slots, T, H,
+                           d, d, k_cache, k_page_stride, k_tok_stride, v_cache, v_page_stride,
+                           v_tok_stride, ts_cache, ts_page_stride, num_pages, page_size, stream);
+    if (st != HSTU_OK) return st;
+    st = hstu_attn_cached_fwd(HSTU_DTYPE_BF16, uvqk + 2 * F, 4 * F, k_cache, k_page_stride, k_tok_stride,
+                              v_cache, v_page_stride, v_tok_stride, ts_cache, ts_page_stride, num_pages,
+                              page_size, block_table, table_stride, max_pages, ctx_lens, new_offsets, B,
+                              T, max_new, H, d, d, timestamps, parents, pos_bias, num_pos, time_bias,
+                              num_time_buckets, max_seqlen, attn, F, ws + w.own, w.total - w.own, stream);
+    if (st != HSTU_OK) return st;
+    // 3. gate, f2 with the residual
+    st = run_ln_gate(attn, F, uvqk, 4 * F, T, F, ln_gamma, ln_beta, ln_eps, ygate, F, s);
+    if (st != HSTU_OK) return st;
+    return project(ygate, F, W2, s2, D, b2, HSTU_EPI_RESIDUAL, x, out);
 }
 
 }  // extern "C"

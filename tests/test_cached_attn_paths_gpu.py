@@ -1,0 +1,154 @@
+"""hstu_attn_cached_fwd where its kernels change over, at odd strides and over
+random batches, against the definition in 64 bits."""
+
+import numpy as np
+import pytest
+import torch
+
+import jagged_pointwise_attention_b200 as hstu
+from jagged_pointwise_attention_b200 import _native
+from serving_util import call_attn, check_attn, make_step, oracle
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def ok():
+    assert hstu.hstu_device_status() == _native.HSTU_OK
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("ctx,new,kind", [
+    ([3000, 1, 77], [1, 1, 1], "chain"), ([3000, 1, 77], [8, 3, 1], "tree"),
+    ([2900, 40], [9, 9], "tree"), ([2900, 40], [16, 2], "siblings"), ([2500, 0], [17, 40], "tree"),
+    ([1800], [64], "tree"), ([1800, 9], [65, 3], "tree"), ([1500, 3], [128, 128], "siblings"),
+    ([900, 60, 0], [200, 129, 256], "tree"), ([200], [700], "chain"), ([127, 128, 129], [130, 128, 1], "chain"),
+    ([250, 255, 100], [5, 1, 8], "tree"), ([1000, 2, 300], [8, 8, 1], "chain"),
+])
+def test_kernels_change_over(ctx, new, kind, d):
+    s = make_step(ctx, new, kind, 2, d, d, 32, BF, seed=d + len(new) + max(new))
+    got = call_attn(hstu, s)
+    ok()
+    check_attn(s, got)
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_many_short_sequences_and_the_same_ones_in_one_long_batch(d):
+    """Enough items that sequences up to 1024 tokens are taken whole, and the
+    same sequences with a longer bound, along the line."""
+    rng = np.random.default_rng(d)
+    ctx = [int(x) for x in rng.integers(0, 700, 160)]
+    new = [int(x) for x in rng.integers(0, 5, 160)]
+    s = make_step(ctx, new, "tree", 2, d, d, 16, BF, seed=d, max_seqlen=1024)
+    a = call_attn(hstu, s)
+    ok()
+    check_attn(s, a)
+    s.max_seqlen = 2048                  # 1 / N is half as large, exactly
+    b = call_attn(hstu, s)
+    ok()
+    check_attn(s, b)
+
+
+@pytest.mark.parametrize("d,n", [(32, 8), (32, 16), (32, 40), (64, 8), (64, 40), (64, 128), (128, 8),
+                                 (128, 64), (128, 120)])
+@pytest.mark.parametrize("long", [False, True])
+@pytest.mark.parametrize("kind", ["tree", "chain"])
+def test_values_that_a_query_does_not_see(d, n, long, kind):
+    """NaN and infinities in keys and values of new tokens reach the queries that
+    see them and no others; around tile and page borders, twice in one page."""
+    s = make_step([1700 if long else 100, 30], [n, 3], kind, 2, d, d, 16, BF, seed=n + d)
+    odd = {1: ("v", float("nan")), 2: ("v", float("inf")), n // 2: ("v", float("-inf")),
+           n - 2: ("k", float("nan")), n - 3: ("v", float("inf"))}
+    for i, (what, x) in odd.items():
+        j = s.ctx[0] + i
+        c = s.kc if what == "k" else s.vc
+        c[int(s.table[0, j // 16]), j % 16, :, 3:9] = x
+    got = call_attn(hstu, s)
+    ok()
+    want, _, _ = oracle(s)
+    g = got.double().cpu().numpy()
+    assert np.array_equal(np.isnan(g), np.isnan(want))
+    inf = np.isinf(want)
+    assert np.array_equal(np.isinf(g), inf) and np.array_equal(g[inf], want[inf])
+    # whole rows that see none of them
+    par = s.parents if s.parents is not None else np.array([i - 1 for i in range(n)] + [-1, 0, 1])
+    clean = []
+    for i in range(n):
+        p, hit = i, False
+        while p >= 0:
+            hit = hit or p in odd
+            p = int(par[p])
+        clean.append(not hit)
+    check_attn(s, got, np.array(clean + [True] * 3))
+    # the finite columns of the others: a value that is not finite leaves them alone
+    fin = np.isfinite(want)
+    rel = np.linalg.norm((g - want)[fin]) / np.linalg.norm(want[fin])
+    assert rel <= 1e-2, rel
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("n", [1, 12, 70])
+def test_page_stride_that_is_no_multiple_of_the_tokens(d, n):
+    H, page = 2, 16
+    s = make_step([600, 33], [n, 1], "tree", H, d, d, page, BF, seed=d + n)
+    pages, row = s.kc.shape[0], H * d + 8
+    store = torch.full((pages * (2 * page * row + 24),), float("nan"), dtype=BF).cuda()
+    views = []
+    for i, c in enumerate((s.kc, s.vc)):
+        v = torch.as_strided(store, (pages, page, H, d), (2 * page * row + 24, row, d, 1), i * page * row + 8)
+        v.copy_(c.cuda())
+        views.append(v)
+    got = call_attn(hstu, s, k_cache=views[0], v_cache=views[1])
+    ok()
+    check_attn(s, got)
+
+
+@pytest.mark.parametrize("n", [1, 20, 100])
+def test_bad_pages_parents_and_sequences(n):
+    """On the tcgen05 kernel: a bad page counts as no tokens, a bad parent as -1,
+    a sequence that cannot be is left out, the others keep their bits."""
+    s = make_step([1500, 700, 90], [n, n, 1], "tree", 2, 64, 64, 16, BF, seed=n)
+    want = call_attn(hstu, s)
+    ok()
+    check_attn(s, want)
+    tab = s.table.copy()
+    tab[0, 3], tab[0, 20] = -1, 2 ** 30
+    got = call_attn(hstu, s, block_table=torch.from_numpy(tab).cuda())
+    assert hstu.hstu_device_status() == _native.HSTU_ERR_BAD_INPUT
+    assert bool(torch.isfinite(got).all()) and torch.equal(got[2 * n:], want[2 * n:])
+    out = torch.full_like(want, 3.0)
+    call_attn(hstu, s, ctx_lens=torch.tensor([1500, 10 ** 9, 90], dtype=torch.int32).cuda(), out=out)
+    assert hstu.hstu_device_status() == _native.HSTU_ERR_BAD_INPUT
+    assert bool((out[n: 2 * n] == 3.0).all())
+    s.ctx, s.new = [1500, 90], [n, 1]
+    keep = list(range(n)) + [2 * n]
+    s.q, s.ts, s.parents, s.table = s.q[keep], s.ts[keep], s.parents[keep], s.table[[0, 2]]
+    check_attn(s, out[keep])
+    if n > 2:
+        bad = s.parents.copy()
+        bad[2] = 2
+        s.parents[2] = -1
+        got = call_attn(hstu, s, parents=torch.from_numpy(bad).cuda())
+        assert hstu.hstu_device_status() == _native.HSTU_ERR_BAD_INPUT
+        check_attn(s, got)
+    ok()
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_batches(seed):
+    rng = np.random.default_rng(1000 + seed)
+    B = int(rng.integers(1, 12))
+    dtype = F32 if seed % 6 == 5 else BF
+    d = int(rng.choice([32, 64, 128]))
+    most = int(rng.choice([1, 3, 8, 16, 60, 130]))
+    ctx = [int(x) for x in np.exp(rng.uniform(0, np.log(1500), B)).astype(int) - 1]
+    new = [int(x) for x in rng.integers(0, most + 1, B)]
+    new[int(rng.integers(0, B))] = most
+    s = make_step(ctx, new, str(rng.choice(["chain", "tree", "siblings", "path"])), int(rng.integers(1, 5)),
+                  d, d, int(rng.choice([16, 32, 64, 128, 256])), dtype, num_pos=int(rng.choice([1, 50, 4000])),
+                  num_buckets=int(rng.choice([3, 30, 128])), seed=seed, use_time=bool(rng.integers(0, 4)),
+                  use_pos=bool(rng.integers(0, 4)), gap=float(rng.choice([0.4, 3600.0, 4e8])))
+    a = call_attn(hstu, s)
+    ok()
+    check_attn(s, a)
+    assert torch.equal(a, call_attn(hstu, s))
