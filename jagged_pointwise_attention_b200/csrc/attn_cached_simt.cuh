@@ -2,11 +2,12 @@
 // cores, fp32 arithmetic (attn_cached.cuh has the formula and the work line).
 //
 // A block of 128 threads takes key tiles of 64 keys for tiles of 8 queries.
-// Scores: the tile's keys are copied to shared memory (rows padded by four
-// floats, so the 16-byte reads of eight lanes fall into different banks);
-// thread t has key t % 64 and four of the eight queries. Values: thread t has
-// column t % DMAX of the output and every (128 / DMAX)-th key, and reads V
-// straight from the cache, coalesced over the columns.
+// A tile's keys, values and timestamps are copied to shared memory at once
+// (cp.async; rows padded by four floats, so the 16-byte reads of eight lanes
+// fall into different banks), its pages looked up a tile ahead: bound by the
+// latency of these copies, with about two tiles a block. Scores: thread t has
+// key t % 64 and four of the eight queries. Values: thread t has column t %
+// DMAX of the output and every (128 / DMAX)-th key.
 #pragma once
 
 #include "attn_cached.cuh"
@@ -21,7 +22,8 @@ constexpr int kSimtBlocks = 4 * 148;
 template <int DMAX>
 struct CachedSimtSmem {
     alignas(16) float q[kSimtRows][DMAX];
-    alignas(16) float k[kSimtKeys][DMAX + 4];
+    alignas(16) float k[kSimtKeys][DMAX + 4];       // columns behind dqk stay zero
+    alignas(16) float v[kSimtKeys][DMAX + 4];
     alignas(16) float p[kSimtKeys][kSimtRows];
     float red[kSimtRows][DMAX];
     int64_t tk[kSimtKeys];
@@ -34,7 +36,7 @@ struct CachedSimtSmem {
     TreeSmem tree;
 };
 
-// VEC: rows are 16-byte aligned and dqk a multiple of four
+// VEC: rows are 16-byte aligned, dqk and dv multiples of four
 template <int DMAX, bool VEC>
 __global__ void __launch_bounds__(kSimtThreads) attn_cached_simt_kernel(const CachedArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -51,6 +53,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_cached_simt_kernel(const Ca
     int64_t left = L::cut(total, blockIdx.x + 1, gridDim.x) - begin;
     if (tid == 0) write_head<kSimtKeys, kSimtRows>(a, at, total, begin);
     if (left <= 0) return;
+    for (int i = tid; i < kSimtKeys * (DMAX + 4); i += kSimtThreads) (&sm.k[0][0])[i] = 0.f;
     const float* qp = static_cast<const float*>(a.q);
     const float* kp = static_cast<const float*>(a.k);
     const float* vp = static_cast<const float*>(a.v);
@@ -83,15 +86,19 @@ __global__ void __launch_bounds__(kSimtThreads) attn_cached_simt_kernel(const Ca
         }
         float acc[kSimtRows] = {};
         const int col = tid % DMAX, grp = tid / DMAX;
+        const int32_t* table = a.table + static_cast<int64_t>(at.b) * a.table_stride;
+        const int64_t hk = static_cast<int64_t>(at.h) * a.dqk, hv = static_cast<int64_t>(at.h) * a.dv;
+        auto look = [&](int key) { return tid < kSimtKeys && key < len ? __ldg(table + (key >> a.shift)) : 0; };
+        int ahead = look(at.j * kSimtKeys + tid);
         for (int j = at.j; j < at.j + take; ++j) {
             const int k0 = j * kSimtKeys, nk = min(kSimtKeys, len - k0);
-            // the tile's keys: page, position, timestamp
+            // the tile's keys: page, position
             __syncthreads();
             if (tid < kSimtKeys) {
                 int page = -1, pk = 0;
                 if (tid < nk) {
                     const int key = k0 + tid;
-                    page = a.table[static_cast<int64_t>(at.b) * a.table_stride + (key >> a.shift)];
+                    page = ahead;
                     if (page < 0 || page >= a.num_pages) {
                         raise_error(kErrBadInput);
                         page = -1;
@@ -100,33 +107,31 @@ __global__ void __launch_bounds__(kSimtThreads) attn_cached_simt_kernel(const Ca
                     if (a.parents != nullptr && key >= at.s.ctx)
                         pk = at.s.ctx + sm.tree.depth[key - at.s.ctx];
                     if (use_time && page >= 0)
-                        sm.tk[tid] = a.tsc[page * a.tsc_page + (key & page_mask)];
+                        cp_async8(&sm.tk[tid], a.tsc + page * a.tsc_page + (key & page_mask));
                 }
                 sm.page[tid] = page;
                 sm.pk[tid] = pk;
             }
             __syncthreads();
-            if (VEC) {
-                const int nv = a.dqk / 4;
-                for (int i = tid; i < kSimtKeys * (DMAX / 4); i += kSimtThreads) {
-                    const int r = i / (DMAX / 4), c = i % (DMAX / 4);
-                    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (sm.page[r] >= 0 && c < nv)
-                        f = *reinterpret_cast<const float4*>(
-                            kp + sm.page[r] * a.k_page + ((k0 + r) & page_mask) * a.k_tok +
-                            static_cast<int64_t>(at.h) * a.dqk + 4 * c);
-                    *reinterpret_cast<float4*>(&sm.k[r][4 * c]) = f;
+            constexpr int W = VEC ? 4 : 1;          // floats a copy
+            const int ck = a.dqk / W, cv = a.dv / W;
+            for (int i = tid; i < kSimtKeys * (DMAX / W); i += kSimtThreads) {
+                const int r = i / (DMAX / W), c = i % (DMAX / W);
+                if (sm.page[r] < 0) continue;
+                const int64_t row = (k0 + r) & page_mask;
+                if (c < ck) {
+                    const float* src = kp + sm.page[r] * a.k_page + row * a.k_tok + hk + W * c;
+                    if (VEC) cp_async16(&sm.k[r][W * c], src);
+                    else cp_async4(&sm.k[r][c], src);
                 }
-            } else {
-                for (int i = tid; i < kSimtKeys * DMAX; i += kSimtThreads) {
-                    const int r = i / DMAX, c = i % DMAX;
-                    float f = 0.f;
-                    if (sm.page[r] >= 0 && c < a.dqk)
-                        f = kp[sm.page[r] * a.k_page + ((k0 + r) & page_mask) * a.k_tok +
-                               static_cast<int64_t>(at.h) * a.dqk + c];
-                    sm.k[r][c] = f;
+                if (c < cv) {
+                    const float* src = vp + sm.page[r] * a.v_page + row * a.v_tok + hv + W * c;
+                    if (VEC) cp_async16(&sm.v[r][W * c], src);
+                    else cp_async4(&sm.v[r][c], src);
                 }
             }
+            ahead = look(k0 + kSimtKeys + tid);
+            cp_async_wait_all();
             __syncthreads();
             // scores of key tid % 64, queries 4 (tid / 64) ..
             {
@@ -170,10 +175,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_cached_simt_kernel(const Ca
             __syncthreads();
             if (col < a.dv) {
                 for (int r = grp; r < nk; r += kGroups) {
-                    const int page = sm.page[r];
-                    if (page < 0) continue;
-                    const float v = vp[page * a.v_page + ((k0 + r) & page_mask) * a.v_tok +
-                                       static_cast<int64_t>(at.h) * a.dv + col];
+                    const float v = sm.v[r][col];
                     // a key that a query does not see adds nothing, whatever its value
                     // is (not 0 * v, which is NaN for a v that is not finite)
                     const uint32_t vis = sm.vis[0][r] | (static_cast<uint32_t>(sm.vis[1][r]) << 4);

@@ -398,8 +398,9 @@ hstu_status_t hstu_attn_cached_fwd(hstu_dtype_t dtype, const void* q, int64_t q_
         if (d_qk == 64) return run_cached_bf16<64>(a, as_stream(stream));
         return run_cached_bf16<128>(a, as_stream(stream));
     }
-    const bool vec = aligned16(k_cache) && k_page_stride % 4 == 0 && k_tok_stride % 4 == 0 &&
-                     d_qk % 4 == 0;
+    const bool vec = aligned16(k_cache) && aligned16(v_cache) && k_page_stride % 4 == 0 &&
+                     k_tok_stride % 4 == 0 && v_page_stride % 4 == 0 && v_tok_stride % 4 == 0 &&
+                     d_qk % 4 == 0 && d_v % 4 == 0;
     return vec ? run_cached_simt<true>(a, as_stream(stream))
                : run_cached_simt<false>(a, as_stream(stream));
 }

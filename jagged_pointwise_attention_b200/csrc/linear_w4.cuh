@@ -54,11 +54,12 @@ constexpr int kW4Pitch = 80;        // bytes of a row in the ring: 64 and 16 aga
 template <int MT>
 constexpr int w4_stage_bytes() { return 16 * MT * kW4Pitch; }
 
+// (b & mask) | magic as one operation; the compiler took two.
 __device__ __forceinline__ uint32_t w4_pair(uint32_t c, int p) {
-    const uint32_t b = ((c >> (4 * p)) & 0x000f000fu) | 0x43004300u;
-    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&b),
-                                     __floats2bfloat162_rn(136.f, 136.f));
-    return *reinterpret_cast<const uint32_t*>(&v);
+    uint32_t b, v;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(b) : "r"(c >> (4 * p)), "r"(0x000f000fu), "r"(0x43004300u));
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(v) : "r"(b), "r"(0x43084308u));
+    return v;
 }
 
 // MT: 16-row tiles of W a block; NT: 8-row tiles of x a block. G: group size.
@@ -117,6 +118,7 @@ __global__ void __launch_bounds__(256) linear_w4_kernel(const LinearW4Args a) {
     };
     ahead(kb0);
     float acc[MT][NT][4] = {};
+#pragma unroll 4
     for (int kb = kb0; kb < kb1; ++kb) {
         float sc[2 * MT][GB];
 #pragma unroll
