@@ -1,12 +1,13 @@
 // attn_cached_simt.cuh -- attention of new tokens over a paged cache on CUDA
 // cores, fp32 arithmetic (attn_cached.cuh has the formula and the work line).
 //
-// A block of 128 threads takes key tiles of 64 keys for tiles of 8 queries.
+// A block of 128 threads takes key tiles of 64 keys for tiles of R queries: 8,
+// or 16 where there are more new tokens (each tile reads its keys again).
 // A tile's keys, values and timestamps are copied to shared memory at once
 // (cp.async; rows padded by four floats, so the 16-byte reads of eight lanes
 // fall into different banks), its pages looked up a tile ahead: bound by the
 // latency of these copies, with about two tiles a block. Scores: thread t has
-// key t % 64 and four of the eight queries. Values: thread t has column t %
+// key t % 64 and half of the queries. Values: thread t has column t %
 // DMAX of the output and every (128 / DMAX)-th key.
 #pragma once
 
@@ -15,34 +16,32 @@
 namespace hstu {
 
 constexpr int kSimtKeys = 64;
-constexpr int kSimtRows = 8;
 constexpr int kSimtThreads = 128;
 constexpr int kSimtBlocks = 4 * 148;
 
-template <int DMAX>
+template <int DMAX, int R>
 struct CachedSimtSmem {
-    alignas(16) float q[kSimtRows][DMAX];
+    alignas(16) float q[R][DMAX];
     alignas(16) float k[kSimtKeys][DMAX + 4];       // columns behind dqk stay zero
     alignas(16) float v[kSimtKeys][DMAX + 4];
-    alignas(16) float p[kSimtKeys][kSimtRows];
-    float red[kSimtRows][DMAX];
+    alignas(16) float p[kSimtKeys][R + 4];
     int64_t tk[kSimtKeys];
-    int64_t tq[kSimtRows];
+    int64_t tq[R];
     int64_t scratch[kSimtThreads / 32 + 8];
     int page[kSimtKeys];            // the key's page (its number in the cache), -1 none
     int pk[kSimtKeys];
-    uint8_t vis[2][kSimtKeys];      // bit i of half h: query 4h + i sees the key
+    uint32_t vis[2][kSimtKeys];     // bit i of half h: query h R / 2 + i sees the key
     float tb[64];
     TreeSmem tree;
 };
 
 // VEC: rows are 16-byte aligned, dqk and dv multiples of four
-template <int DMAX, bool VEC>
+template <int DMAX, int R, bool VEC>
 __global__ void __launch_bounds__(kSimtThreads) attn_cached_simt_kernel(const CachedArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    using S = CachedSimtSmem<DMAX>;
+    using S = CachedSimtSmem<DMAX, R>;
     S& sm = *reinterpret_cast<S*>(smem_raw);
-    using L = Line<kSimtKeys, kSimtRows>;
+    using L = Line<kSimtKeys, R>;
     constexpr int kGroups = kSimtThreads / DMAX;        // key groups of the value pass
     const int tid = threadIdx.x;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -51,7 +50,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_cached_simt_kernel(const Ca
                                                            blockIdx.x == 0);
     const int64_t begin = L::cut(total, blockIdx.x, gridDim.x);
     int64_t left = L::cut(total, blockIdx.x + 1, gridDim.x) - begin;
-    if (tid == 0) write_head<kSimtKeys, kSimtRows>(a, at, total, begin);
+    if (tid == 0) write_head<kSimtKeys, R>(a, at, total, begin);
     if (left <= 0) return;
     for (int i = tid; i < kSimtKeys * (DMAX + 4); i += kSimtThreads) (&sm.k[0][0])[i] = 0.f;
     const float* qp = static_cast<const float*>(a.q);
@@ -64,15 +63,15 @@ __global__ void __launch_bounds__(kSimtThreads) attn_cached_simt_kernel(const Ca
     while (left > 0) {
         const int nt = L::tiles(at.s, at.qt);
         const int take = static_cast<int>(min(left, static_cast<int64_t>(nt - at.j)));
-        const int q0 = at.qt * kSimtRows;
-        const int rows = min(kSimtRows, at.s.n - q0);
-        const int len = at.s.ctx + min(at.s.n, q0 + kSimtRows);
+        const int q0 = at.qt * R;
+        const int rows = min(R, at.s.n - q0);
+        const int len = at.s.ctx + min(at.s.n, q0 + R);
         if (a.parents != nullptr && tree_of != at.b) {
             build_tree(a, at.s, sm.tree, tid, kSimtThreads, [] { __syncthreads(); });
             tree_of = at.b;
         }
         __syncthreads();
-        for (int i = tid; i < kSimtRows * DMAX; i += kSimtThreads) {
+        for (int i = tid; i < R * DMAX; i += kSimtThreads) {
             const int r = i / DMAX, c = i % DMAX;
             float f = 0.f;
             if (r < rows && c < a.dqk)
@@ -84,7 +83,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_cached_simt_kernel(const Ca
             if (tid < 64) sm.tb[tid] = a.tb[static_cast<int64_t>(at.h) * a.NB + min(tid, a.NB - 1)];
             head_of = at.h;
         }
-        float acc[kSimtRows] = {};
+        float acc[R] = {};
         const int col = tid % DMAX, grp = tid / DMAX;
         const int32_t* table = a.table + static_cast<int64_t>(at.b) * a.table_stride;
         const int64_t hk = static_cast<int64_t>(at.h) * a.dqk, hv = static_cast<int64_t>(at.h) * a.dv;
@@ -135,12 +134,13 @@ __global__ void __launch_bounds__(kSimtThreads) attn_cached_simt_kernel(const Ca
             __syncthreads();
             // scores of key tid % 64, queries 4 (tid / 64) ..
             {
-                const int r = tid % kSimtKeys, i0 = (tid / kSimtKeys) * 4;
-                float s[4] = {};
+                constexpr int HALF = R / 2;
+                const int r = tid % kSimtKeys, half = tid / kSimtKeys, i0 = half * HALF;
+                float s[HALF] = {};
                 for (int c = 0; c < a.dqk; c += 4) {
                     const float4 kv = *reinterpret_cast<const float4*>(&sm.k[r][c]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < HALF; ++i) {
                         const float4 qv = *reinterpret_cast<const float4*>(&sm.q[i0 + i][c]);
                         s[i] = fmaf(kv.x, qv.x, s[i]);
                         s[i] = fmaf(kv.y, qv.y, s[i]);
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_cached_simt_kernel(const Ca
                 const int m = k0 + r - at.s.ctx;        // new token's index, < 0: cached
                 uint32_t vis = 0u;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < HALF; ++i) {
                     const int qi = q0 + i0 + i;
                     bool see = sm.page[r] >= 0 && i0 + i < rows;
                     if (m >= 0)
@@ -170,33 +170,46 @@ __global__ void __launch_bounds__(kSimtThreads) attn_cached_simt_kernel(const Ca
                     }
                     sm.p[r][i0 + i] = p;
                 }
-                sm.vis[i0 / 4][r] = static_cast<uint8_t>(vis);
+                sm.vis[half][r] = vis;
             }
             __syncthreads();
             if (col < a.dv) {
+                const uint32_t every = 0xffffffffu >> (32 - rows);
                 for (int r = grp; r < nk; r += kGroups) {
                     const float v = sm.v[r][col];
-                    // a key that a query does not see adds nothing, whatever its value
-                    // is (not 0 * v, which is NaN for a v that is not finite)
-                    const uint32_t vis = sm.vis[0][r] | (static_cast<uint32_t>(sm.vis[1][r]) << 4);
+                    const uint32_t vis = sm.vis[0][r] | (sm.vis[1][r] << (R / 2));
+                    if (vis == every) {
 #pragma unroll
-                    for (int i = 0; i < kSimtRows; ++i)
-                        if ((vis >> i) & 1u) acc[i] = fmaf(sm.p[r][i], v, acc[i]);
+                        for (int i = 0; i < R; i += 4) {
+                            const float4 p = *reinterpret_cast<const float4*>(&sm.p[r][i]);
+                            acc[i] = fmaf(p.x, v, acc[i]);
+                            acc[i + 1] = fmaf(p.y, v, acc[i + 1]);
+                            acc[i + 2] = fmaf(p.z, v, acc[i + 2]);
+                            acc[i + 3] = fmaf(p.w, v, acc[i + 3]);
+                        }
+                    } else {
+                        // a key that a query does not see adds nothing, whatever its value
+                        // is (not 0 * v, which is NaN for a v that is not finite)
+#pragma unroll
+                        for (int i = 0; i < R; ++i)
+                            if ((vis >> i) & 1u) acc[i] = fmaf(sm.p[r][i], v, acc[i]);
+                    }
                 }
             }
         }
+        float(*red)[DMAX] = reinterpret_cast<float(*)[DMAX]>(&sm.v[0][0]);    // V has been read by then
         // sum over the key groups, then the rows (or this block's part of them)
         if (kGroups > 1) {
             for (int g = 1; g < kGroups; ++g) {
                 __syncthreads();
                 if (grp == g) {
 #pragma unroll
-                    for (int i = 0; i < kSimtRows; ++i) sm.red[i][col] = acc[i];
+                    for (int i = 0; i < R; ++i) red[i][col] = acc[i];
                 }
                 __syncthreads();
                 if (grp == 0) {
 #pragma unroll
-                    for (int i = 0; i < kSimtRows; ++i) acc[i] += sm.red[i][col];
+                    for (int i = 0; i < R; ++i) acc[i] += red[i][col];
                 }
             }
         }
@@ -205,7 +218,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_cached_simt_kernel(const Ca
             float* part = a.parts + (2 * static_cast<int64_t>(blockIdx.x) + (first_item ? 0 : 1)) *
                                         a.part_rows * a.dv;
 #pragma unroll
-            for (int i = 0; i < kSimtRows; ++i) {
+            for (int i = 0; i < R; ++i) {
                 if (i >= rows) break;
                 if (whole)
                     static_cast<float*>(a.out)[(at.s.off + q0 + i) * a.out_stride +

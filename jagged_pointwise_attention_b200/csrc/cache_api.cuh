@@ -79,22 +79,28 @@ hstu_status_t launch_join(const CachedArgs& a, cudaStream_t stream) {
     return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }
 
-template <int DMAX, bool VEC>
+template <int DMAX, int R, bool VEC>
 hstu_status_t launch_cached_simt(const CachedArgs& a, cudaStream_t stream) {
     static int done[kMaxDevices] = {0};
-    constexpr int smem = static_cast<int>(sizeof(CachedSimtSmem<DMAX>));
-    if (!ensure_smem(attn_cached_simt_kernel<DMAX, VEC>, smem, done)) return HSTU_ERR_CUDA;
-    attn_cached_simt_kernel<DMAX, VEC><<<kSimtBlocks, kSimtThreads, smem, stream>>>(a);
+    constexpr int smem = static_cast<int>(sizeof(CachedSimtSmem<DMAX, R>));
+    if (!ensure_smem(attn_cached_simt_kernel<DMAX, R, VEC>, smem, done)) return HSTU_ERR_CUDA;
+    attn_cached_simt_kernel<DMAX, R, VEC><<<kSimtBlocks, kSimtThreads, smem, stream>>>(a);
     const hstu_status_t st = launch_status();
     return st == HSTU_OK ? launch_join<1, float, kSimtBlocks>(a, stream) : st;
+}
+
+template <int DMAX, bool VEC>
+hstu_status_t run_cached_simt_rows(const CachedArgs& a, cudaStream_t stream) {
+    return a.max_new <= 8 ? launch_cached_simt<DMAX, 8, VEC>(a, stream)
+                          : launch_cached_simt<DMAX, 16, VEC>(a, stream);
 }
 
 template <bool VEC>
 hstu_status_t run_cached_simt(const CachedArgs& a, cudaStream_t stream) {
     const int d = a.dqk > a.dv ? a.dqk : a.dv;
-    if (d <= 32) return launch_cached_simt<32, VEC>(a, stream);
-    if (d <= 64) return launch_cached_simt<64, VEC>(a, stream);
-    return launch_cached_simt<128, VEC>(a, stream);
+    if (d <= 32) return run_cached_simt_rows<32, VEC>(a, stream);
+    if (d <= 64) return run_cached_simt_rows<64, VEC>(a, stream);
+    return run_cached_simt_rows<128, VEC>(a, stream);
 }
 
 // bf16 [pages, page_size, H d] of a cache, boxes of `rows` tokens x 64 (32) columns.
@@ -158,8 +164,7 @@ hstu_status_t launch_cached_tc(const CachedArgs& a, cudaStream_t stream) {
 
 // Rows of a part: the most that an item of the kernels below can have.
 int cached_part_rows(hstu_dtype_t dtype, int32_t max_new, int32_t d) {
-    if (dtype == HSTU_DTYPE_F32) return kSimtRows;
-    const int most = d == 32 ? 32 : 128;
+    const int most = dtype == HSTU_DTYPE_F32 ? 16 : d == 32 ? 32 : 128;
     return max_new >= most ? most : (max_new + 7) / 8 * 8;
 }
 
