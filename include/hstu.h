@@ -484,7 +484,9 @@ hstu_status_t hstu_cache_append(hstu_dtype_t dtype, const void* k, int64_t k_str
  * impossible numbers (longer than max_seqlen or its table row, more new tokens
  * than max_new) is left out, a page outside the cache counts as no tokens, a
  * parent that is not before its token counts as -1; all report
- * HSTU_ERR_BAD_INPUT. Results are the same bits on every run. Two launches. */
+ * HSTU_ERR_BAD_INPUT. Pages may be shared by sequences (a common prefix).
+ * Results are the same bits on every run. One launch, or two where sequences
+ * may be split over blocks. */
 size_t hstu_attn_cached_workspace_bytes(hstu_dtype_t dtype, int32_t max_new, int32_t d_v);
 hstu_status_t hstu_attn_cached_fwd(hstu_dtype_t dtype, const void* q, int64_t q_tok_stride,
                                    const void* k_cache, int64_t k_page_stride,
@@ -519,8 +521,8 @@ hstu_status_t hstu_quant_groups_w4(const void* W, int64_t ldw, int64_t N, int32_
  * weights' bytes. Codes and scales as hstu_quant_groups_w4 writes them; x, y,
  * residual bf16, bias fp32 [N] or NULL, epilogues as hstu_linear_fwd. Products
  * are exact in fp32 before the scale, sums are fp32, and the result is rounded
- * once. K % 128 == 0, any N >= 1; x and codes 16-byte aligned, ldx % 8 == 0,
- * ldc % 16 == 0. For many rows hstu_linear_fwd and hstu_linear_fp8_fwd are the
+ * once. K % 128 == 0, 1 <= N <= 2^31 - 65; x and codes 16-byte aligned, ldx % 8
+ * == 0, ldc % 16 == 0. For many rows hstu_linear_fwd and hstu_linear_fp8_fwd are the
  * faster calls: the weights are read once for every 64 rows. */
 hstu_status_t hstu_linear_w4_fwd(const void* x, int64_t ldx, int64_t M, int32_t K, const void* codes,
                                  int64_t ldc, const void* scales, int64_t lds, int32_t group,

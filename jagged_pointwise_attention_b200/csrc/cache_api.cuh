@@ -51,7 +51,8 @@ hstu_status_t validate_cached(hstu_dtype_t dtype, const CachedArgs& c, int32_t p
         return HSTU_ERR_INVALID_ARG;
     if (c.k_page < (page_size - 1) * c.k_tok + rq || c.v_page < (page_size - 1) * c.v_tok + rv)
         return HSTU_ERR_INVALID_ARG;
-    if (c.tsc && c.tsc_page < page_size) return HSTU_ERR_INVALID_ARG;
+    if (c.tsc && (c.tsc_page < page_size || reinterpret_cast<uintptr_t>(c.tsc) % 8))
+        return HSTU_ERR_INVALID_ARG;
     if (dtype == HSTU_DTYPE_BF16) {
         if (!aligned16(c.q) || !aligned16(c.k) || !aligned16(c.v) || !aligned16(c.out))
             return HSTU_ERR_INVALID_ARG;
@@ -307,7 +308,8 @@ hstu_status_t hstu_cache_append(hstu_dtype_t dtype, const void* k, int64_t k_str
         v_page_stride < (page_size - 1) * v_tok_stride + rv)
         return HSTU_ERR_INVALID_ARG;
     if ((timestamps == nullptr) != (ts_cache == nullptr)) return HSTU_ERR_INVALID_ARG;
-    if (ts_cache && ts_page_stride < page_size) return HSTU_ERR_INVALID_ARG;
+    if (ts_cache && (ts_page_stride < page_size || reinterpret_cast<uintptr_t>(ts_cache) % 8))
+        return HSTU_ERR_INVALID_ARG;
     if (total_new == 0) return HSTU_OK;
     if (!k || !v || !slots || !k_cache || !v_cache) return HSTU_ERR_INVALID_ARG;
     if (total_new > 1 && (k_stride < rk || v_stride < rv)) return HSTU_ERR_INVALID_ARG;
@@ -441,7 +443,7 @@ hstu_status_t hstu_linear_w4_fwd(const void* x, int64_t ldx, int64_t M, int32_t 
     if (M < 0 || K < 1 || N < 1) return HSTU_ERR_INVALID_ARG;
     if (epilogue != HSTU_EPI_NONE && epilogue != HSTU_EPI_SILU && epilogue != HSTU_EPI_RESIDUAL)
         return HSTU_ERR_INVALID_ARG;
-    if ((group != 32 && group != 64 && group != 128) || K % 128 || M > 65535 * 8)
+    if ((group != 32 && group != 64 && group != 128) || K % 128 || M > 65535 * 8 || N > 0x7fffffff - 64)
         return HSTU_ERR_UNSUPPORTED;
     if (M == 0) return HSTU_OK;
     if (!x || !codes || !scales || !y || (epilogue == HSTU_EPI_RESIDUAL && !residual))

@@ -48,6 +48,12 @@ __device__ __forceinline__ void w4_store(const LinearW4Args& a, int64_t m, int n
 // plain fp32; the scale multiplies the group's sum. The order of k inside a
 // fragment is free as long as W and x share it: nibbles i and i + 4 of a word
 // are one register, and x is paired to match.
+//
+// 16384 x 8192 weights, eight rows: 26.6 us, 2.6 TB/s of codes, scales and x.
+// By then the bound is the unpacking: eleven operations for eight codes, seven
+// of them on the integer pipe at half rate, which is 0.55 busy over the launch.
+// Four row tiles a warp (29 us), two or eight warps a block (31 us), six stages
+// (36 us) and x not loaded ahead (33 us) were slower.
 constexpr int kW4Stages = 4;
 constexpr int kW4Pitch = 80;        // bytes of a row in the ring: 64 and 16 against bank conflicts
 
