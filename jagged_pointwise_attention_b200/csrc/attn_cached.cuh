@@ -270,34 +270,52 @@ __device__ __forceinline__ void store_out(__nv_bfloat16* dst, const float (&v)[4
 // by the lengths.
 constexpr int kJoinWarps = 8;
 constexpr int kJoinThreads = kJoinWarps * 32;
-constexpr int kJoinBlocks = 3 * 148;
+constexpr int kJoinBlocks = 6 * 148;
 constexpr int kJoinFew = 6;
+
+// An item as the units of the join need it.
+struct JoinItem {
+    int64_t row;                                // first row of out
+    int32_t c, parts;                           // the parts are those of blocks c - 1 ..
+    int32_t first;                              // index of the part of block c - 1
+    int32_t rows, h;
+};
 
 template <int V, typename TOut, int BLOCKS>
 __global__ void __launch_bounds__(kJoinThreads) attn_cached_join_kernel(const CachedArgs a) {
-    __shared__ int cuts[2][BLOCKS];             // few, many
+    __shared__ JoinItem items[BLOCKS];          // few parts from the front, many from the back
     __shared__ int warp_n[2][kJoinWarps];
     __shared__ float sums[kJoinWarps][32 * V];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t total = a.heads[0].total;
-    // blocks that share the item at cut c: c - 1 .. this one
-    auto last_of = [&](const PartHead& p) {
-        return min(BLOCKS - 1, static_cast<int>(((p.start + p.tiles) * BLOCKS - 1) / total));
-    };
     int n[2] = {0, 0};
     for (int c0 = 1; c0 < BLOCKS; c0 += kJoinThreads) {
         const int c = c0 + tid;
         bool is = false, many = false;
+        JoinItem item;
         if (c < BLOCKS) {
             const PartHead p = a.heads[c];
-            is = p.tiles > 0 && line_cut(total, c, BLOCKS) != p.start &&
-                 line_cut(total, c - 1, BLOCKS) <= p.start;
-            many = is && last_of(p) - c + 2 > kJoinFew;
+            const int64_t before = line_cut(total, c - 1, BLOCKS);
+            is = p.tiles > 0 && line_cut(total, c, BLOCKS) != p.start && before <= p.start;
+            if (is) {
+                // the last block whose part begins inside; c - 1's part is its last
+                // item's, its only one's when it begins with this item
+                const int64_t end = (p.start + p.tiles) * BLOCKS - 1;
+                const int last = total < (1 << 20) ? static_cast<uint32_t>(end) / static_cast<uint32_t>(total)
+                                                   : static_cast<int>(end / total);
+                item.row = p.row;
+                item.c = c;
+                item.parts = min(BLOCKS - 1, last) - c + 2;
+                item.first = 2 * (c - 1) + (before != p.start ? 1 : 0);
+                item.rows = p.rows;
+                item.h = p.h;
+                many = item.parts > kJoinFew;
+            }
         }
         const uint32_t m[2] = {__ballot_sync(0xffffffffu, is && !many),
                                __ballot_sync(0xffffffffu, many)};
-        __syncthreads();
+        if (BLOCKS > kJoinThreads) __syncthreads();
         if (lane < 2) warp_n[lane][warp] = __popc(m[lane]);
         __syncthreads();
 #pragma unroll
@@ -308,34 +326,33 @@ __global__ void __launch_bounds__(kJoinThreads) attn_cached_join_kernel(const Ca
                 if (w < warp) at += warp_n[k][w];
                 n[k] += warp_n[k][w];
             }
-            if (is && many == (k == 1)) cuts[k][at + __popc(m[k] & ((1u << lane) - 1u))] = c;
+            at += __popc(m[k] & ((1u << lane) - 1u));
+            if (is && many == (k == 1)) items[k == 0 ? at : BLOCKS - 1 - at] = item;
         }
     }
     __syncthreads();
     const int values = a.part_rows * a.dv;
     const int per_few = (values + kJoinThreads * V - 1) / (kJoinThreads * V);
     const int per_many = (values + 32 * V - 1) / (32 * V);
-    for (int u = blockIdx.x; u < n[0] * per_few + n[1] * per_many; u += gridDim.x) {
-        const bool many = u >= n[0] * per_few;
-        const int x = many ? u - n[0] * per_few : u;
-        const int c = many ? cuts[1][x / per_many] : cuts[0][x / per_few];
-        const PartHead p = a.heads[c];
-        const int i = (many ? x % per_many * 32 + lane : x % per_few * kJoinThreads + tid) * V;
+    const int few_units = n[0] * per_few, units = few_units + n[1] * per_many;
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+        const bool many = u >= few_units;
+        const int x = many ? u - few_units : u, per = many ? per_many : per_few;
+        const int at = x / per, piece = x - at * per;
+        const JoinItem& p = items[many ? BLOCKS - 1 - at : at];
+        const int i = (many ? piece * 32 + lane : piece * kJoinThreads + tid) * V;
         const bool live = i < p.rows * a.dv;
-        const int parts = last_of(p) - c + 2;
-        const int q0 = many ? parts * warp / kJoinWarps : 0;
-        const int q1 = many ? parts * (warp + 1) / kJoinWarps : parts;
+        const int q0 = many ? p.parts * warp / kJoinWarps : 0;
+        const int q1 = many ? p.parts * (warp + 1) / kJoinWarps : p.parts;
         float v[V] = {};
         const float* src = a.parts + i;
 #pragma unroll 4
         for (int q = q0; q < q1; ++q) {
-            const int b = c - 1 + q;
-            // (with fewer tiles than blocks some have none)
+            // (with fewer tiles than blocks some blocks have none)
+            const int b = p.c - 1 + q;
             const bool has = live && (total >= BLOCKS ||
                                       line_cut(total, b, BLOCKS) < line_cut(total, b + 1, BLOCKS));
-            // c - 1's part is its last item's, its only one's when it begins with this item
-            const int part = 2 * b + (q == 0 && line_cut(total, b, BLOCKS) != p.start ? 1 : 0);
-            const float* s = src + static_cast<int64_t>(part) * values;
+            const float* s = src + static_cast<int64_t>(q == 0 ? p.first : 2 * b) * values;
             if constexpr (V == 4) {
                 const float4 f = has ? *reinterpret_cast<const float4*>(s) : make_float4(0.f, 0.f, 0.f, 0.f);
                 v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
