@@ -1,6 +1,8 @@
 // attn_cached.cuh -- attention of new tokens over a paged cache: the work
-// line, the tree of new tokens and the join, shared by the bf16 and the fp32
-// kernel.
+// line, the tree of new tokens and the join, shared by the kernels: bf16 on
+// tcgen05 (attn_cached_tc.cuh) and, for short sequences and heads of 32, on
+// warp products (attn_cached_mma.cuh), fp32 on CUDA cores
+// (attn_cached_simt.cuh).
 //
 //   out_i = (1/N) sum_{j seen by i} silu(q_i.k_j + pos[p_i - p_j]
 //                                        + time[bucket(t_i - t_j)]) v_j

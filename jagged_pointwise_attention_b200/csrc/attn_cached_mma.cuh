@@ -1,4 +1,4 @@
-// attn_cached_mma.cuh -- attention of up to eight new tokens over short paged
+// attn_cached_mma.cuh -- attention of up to sixteen new tokens over short paged
 // sequences, which a block takes whole, and of heads of 32, bf16
 // (attn_cached.cuh has the formula and the work line).
 //

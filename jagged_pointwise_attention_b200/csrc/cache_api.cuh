@@ -178,11 +178,15 @@ int64_t cached_whole_items(const CachedArgs& a, int rows) {
 }
 
 // Heads of 64 and 128: the tcgen05 kernel, but for up to eight new tokens over
-// short sequences.
+// sequences that are taken whole, and up to sixteen over those of up to 256
+// tokens. (300 sequences of 200, 12 new tokens, 2 heads of 128: 36 us against
+// 43, 4 of 64: 36 and 61; of 900, 16 new tokens, heads of 128: 61 and 46.)
 template <int D>
 hstu_status_t run_cached_bf16(const CachedArgs& a, cudaStream_t stream) {
-    const int64_t items = cached_whole_items(a, 8);
+    const int64_t items = cached_whole_items(a, a.max_new <= 8 ? 8 : 16);
     if (a.max_new <= 8 && items) return launch_cached_mma<D, 1, true>(a, items, stream);
+    if (a.max_new <= 16 && a.max_seqlen <= kWholeLen && items)
+        return launch_cached_mma<D, 2, true>(a, items, stream);
     return a.max_new <= 64 ? launch_cached_tc<D, 64>(a, stream) : launch_cached_tc<D, 128>(a, stream);
 }
 
