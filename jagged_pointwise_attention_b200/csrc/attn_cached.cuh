@@ -15,7 +15,9 @@
 // ceil(len / KT) key tiles, len = ctx + min(n, (qt + 1) NQ) (no new token sees
 // a later one). The key tiles of all items, in that order, form one line, and
 // block c of the grid takes an equal, contiguous part of it, so long and short
-// sequences and any batch load all blocks alike. There is no softmax, so an
+// sequences and any batch load all blocks alike. (Where ending an item costs a
+// block about as much as E tiles, the line has E more places behind each
+// item's tiles, at which there is nothing to do.) There is no softmax, so an
 // item that several blocks share is their plain sum: each writes its part (32
 // bits) to the workspace and a second, small launch adds the parts in line
 // order -- no atomics, the same bits on every run. Every block finds its part
@@ -122,7 +124,7 @@ __device__ __forceinline__ CachedSeq cached_seq(const CachedArgs& a, int b, bool
 
 // Position on the line.
 struct LineAt {
-    int b, qt, h, j;                // j: key tile within the item
+    int b, qt, h, j;                // j: key tile within the item (from its tiles on: none)
     CachedSeq s;
 };
 
@@ -134,15 +136,15 @@ __device__ __forceinline__ int64_t line_cut(int64_t total, int c, int blocks) {
     return total * c / blocks;
 }
 
-template <int KT, int NQ>
+template <int KT, int NQ, int E = 0>
 struct Line {
     static __device__ __forceinline__ int tiles(const CachedSeq& s, int qt) {
         return (s.ctx + min(s.n, (qt + 1) * NQ) + KT - 1) / KT;
     }
-    // key tiles of one head of sequence s
+    // places of one head of sequence s
     static __device__ __forceinline__ int64_t per_head(const CachedSeq& s) {
         int64_t w = 0;
-        for (int qt = 0; qt * NQ < s.n; ++qt) w += tiles(s, qt);
+        for (int qt = 0; qt * NQ < s.n; ++qt) w += tiles(s, qt) + E;
         return w;
     }
     static __device__ __forceinline__ int64_t cut(int64_t total, int c, int blocks) {
@@ -196,11 +198,11 @@ struct Line {
             }
             int64_t r = x - lo;
             int qt = 0;
-            while (r >= static_cast<int64_t>(tiles(s, qt)) * a.H) {
-                r -= static_cast<int64_t>(tiles(s, qt)) * a.H;
+            while (r >= static_cast<int64_t>(tiles(s, qt) + E) * a.H) {
+                r -= static_cast<int64_t>(tiles(s, qt) + E) * a.H;
                 ++qt;
             }
-            const int nt = tiles(s, qt);
+            const int nt = tiles(s, qt) + E;
             int64_t* f = scratch + THREADS / 32;
             f[0] = b;
             f[1] = qt;
@@ -240,7 +242,7 @@ struct Line {
 };
 
 // Called by one thread of every block, also of those without work.
-template <int KT, int NQ>
+template <int KT, int NQ, int E = 0>
 __device__ __forceinline__ void write_head(const CachedArgs& a, const LineAt& at, int64_t total,
                                            int64_t begin) {
     PartHead p;
@@ -249,7 +251,8 @@ __device__ __forceinline__ void write_head(const CachedArgs& a, const LineAt& at
     if (begin < total) {
         p.start = begin - at.j;
         p.row = at.s.off + at.qt * NQ;
-        p.tiles = Line<KT, NQ>::tiles(at.s, at.qt);
+        p.tiles = Line<KT, NQ, E>::tiles(at.s, at.qt);
+        if (at.j >= p.tiles) p.tiles = 0;
         p.rows = min(NQ, at.s.n - at.qt * NQ);
         p.h = at.h;
     }
@@ -283,7 +286,8 @@ struct JoinItem {
     int32_t rows, h;
 };
 
-template <int V, typename TOut, int BLOCKS>
+// E: as the line's.
+template <int V, typename TOut, int BLOCKS, int E>
 __global__ void __launch_bounds__(kJoinThreads) attn_cached_join_kernel(const CachedArgs a) {
     __shared__ JoinItem items[BLOCKS];          // few parts from the front, many from the back
     __shared__ int warp_n[2][kJoinWarps];
@@ -302,14 +306,15 @@ __global__ void __launch_bounds__(kJoinThreads) attn_cached_join_kernel(const Ca
             is = p.tiles > 0 && line_cut(total, c, BLOCKS) != p.start && before <= p.start;
             if (is) {
                 // the last block whose part begins inside; c - 1's part is its last
-                // item's, its only one's when it begins with this item
+                // item's, its first one's when it begins with this item (or in the
+                // empty places right before it)
                 const int64_t end = (p.start + p.tiles) * BLOCKS - 1;
                 const int last = total < (1 << 20) ? static_cast<uint32_t>(end) / static_cast<uint32_t>(total)
                                                    : static_cast<int>(end / total);
                 item.row = p.row;
                 item.c = c;
                 item.parts = min(BLOCKS - 1, last) - c + 2;
-                item.first = 2 * (c - 1) + (before != p.start ? 1 : 0);
+                item.first = 2 * (c - 1) + (before + E < p.start ? 1 : 0);
                 item.rows = p.rows;
                 item.h = p.h;
                 many = item.parts > kJoinFew;

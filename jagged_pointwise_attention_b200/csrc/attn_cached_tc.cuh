@@ -35,9 +35,9 @@
 //
 // Bound by the cache's bytes for few queries, from about 64 on by the pointwise
 // stage (two SFU operations and about fourteen others a pair). 32 sequences of
-// 256 to 4096 tokens, 4 heads of 128, with the join: 8 new tokens 43 us, 32 47,
-// 64 61, 128 103, against 23 us for the bytes (150 MB) alone. One token over 16
-// sequences of up to 8192: 44 us (180 MB, 4.1 TB/s). Start-up to the first
+// 256 to 4096 tokens, 4 heads of 128, with the join: 8 new tokens 42 us, 32 44,
+// 64 53, 128 89, against 23 us for the bytes (150 MB) alone. One token over 16
+// sequences of up to 8192: 43 us (180 MB, 4.2 TB/s). Start-up to the first
 // product takes about 7 us, the join 3 to 5. Sixteen pointwise warps gained a
 // tenth at 128 queries and lost as much at one; the approximate tanh would save
 // one of the two SFU operations and miss silu's bf16 step.
@@ -51,12 +51,15 @@ constexpr int kTcKeys = 128;
 constexpr int kTcPointWarps = 8;
 constexpr int kTcThreads = (kTcPointWarps + 4 + 7) * 32;
 constexpr int kTcItems = 8;             // ring of published items
+// What an item's end costs a block, in steps (64-token trees 59 us with none, 54
+// with one, 53 with two and three; 128 new tokens 99, 93, 89, 88).
+constexpr int kTcEnd = 2;
 
 // An item of the block's part of the line.
 struct alignas(8) TcItem {
     int64_t row0;                       // first row of q and out
     int32_t b, h, ctx, n, q0;           // q0: first query, among the new tokens
-    int32_t tile, take;                 // first key tile, how many are this block's
+    int32_t tile, take;                 // first key tile, how many are this block's (0: the end)
     int32_t whole;                      // the block has all of them
 };
 
@@ -204,7 +207,7 @@ attn_cached_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                       const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CachedArgs a) {
     using S = CachedTcSmem<D, NQ>;
-    using L = Line<kTcKeys, NQ>;
+    using L = Line<kTcKeys, NQ, kTcEnd>;
     constexpr int NK = S::kK, NV = S::kV, NT = S::kTimes;
     constexpr int kWarpOut = kTcPointWarps, kWarpK = kWarpOut + 4, kWarpV = kWarpK + 1,
                   kWarpS = kWarpV + 1, kWarpO = kWarpS + 1, kWarpWalk = kWarpO + 1,
@@ -273,14 +276,17 @@ attn_cached_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
     const int64_t total = L::template locate<kTcThreads>(
         a, blockIdx.x, gridDim.x, reinterpret_cast<int64_t*>(smem + S::kOffWin), at, blockIdx.x == 0);
     const int64_t begin = L::cut(total, blockIdx.x, gridDim.x);
-    const int64_t steps64 = L::cut(total, blockIdx.x + 1, gridDim.x) - begin;
-    if (tid == 0) write_head<kTcKeys, NQ>(a, at, total, begin);
-    if (steps64 <= 0) return;
-    if (steps64 > INT32_MAX) {              // days of work
+    int64_t left = L::cut(total, blockIdx.x + 1, gridDim.x) - begin;    // of the block's part
+    if (tid == 0) write_head<kTcKeys, NQ, kTcEnd>(a, at, total, begin);
+    if (left > INT32_MAX) {                 // days of work
         if (tid == 0) raise_error(kErrBadInput);
         return;
     }
-    const int steps = static_cast<int>(steps64);
+    if (left > 0 && at.j >= L::tiles(at.s, at.qt)) {    // it begins behind an item's tiles
+        left -= L::tiles(at.s, at.qt) + kTcEnd - at.j;
+        if (left > 0) L::next_item(a, at);
+    }
+    if (left <= 0) return;
     if (warp == kWarpS) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
@@ -308,10 +314,10 @@ attn_cached_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
 
     if (warp == kWarpWalk) {
         // ------------------------------------------------------------ the walk
-        int left = steps;
         for (int n = 0;; ++n) {
             if (n >= kTcItems && !wait(&item_empty[ip.s], ip.phase ^ 1u)) break;
-            const int nt = L::tiles(at.s, at.qt), take = min(left, nt - at.j);
+            const int nt = left > 0 ? L::tiles(at.s, at.qt) : 0;
+            const int take = static_cast<int>(min(left, static_cast<int64_t>(nt - at.j)));
             if (lane == 0) {
                 TcItem& I = items[ip.s];
                 I.row0 = at.s.off + at.qt * NQ;
@@ -325,10 +331,11 @@ attn_cached_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                 I.whole = take == nt;
                 mbar_arrive(&item_full[ip.s]);
             }
+            if (take == 0) break;           // the end: nothing is left
             ip.next();
-            left -= take;
-            if (left <= 0) break;
-            L::next_item(a, at);
+            left -= take + kTcEnd;
+            if (left > 0) L::next_item(a, at);
+            else left = at.j = 0;
         }
     } else if (warp == kWarpK || warp == kWarpV) {
         // ------------------------------------------------------------ K (and timestamps), V
@@ -343,9 +350,9 @@ attn_cached_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         uint32_t phase = 1;                 // of the slot's last use: none is waited for at first
         TcPlace<NT> tp;
         bool ok = true;
-        while (ok && loads < steps) {
+        while (ok) {
             ok = wait(&item_full[ip.s], ip.phase);
-            if (!ok) break;
+            if (!ok || items[ip.s].take == 0) break;
             const TcItem& I = items[ip.s];
             const int take = I.take, len = item_len(I), x0 = I.h * D, part0 = item_part0(I);
             const int32_t* table = a.table + static_cast<int64_t>(I.b) * a.table_stride;
@@ -412,10 +419,10 @@ attn_cached_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         // ------------------------------------------------------------ Q and the tables
         int16_t* parent = reinterpret_cast<int16_t*>(trees + 2);
         int it = 0, queries = 0;            // items, loads of Q
-        for (int i = 0; i < steps; ++it) {
-            if (!wait(&item_full[ip.s], ip.phase)) break;
+        for (;; ++it) {
+            if (!wait(&item_full[ip.s], ip.phase) || items[ip.s].take == 0) break;
             const TcItem& I = items[ip.s];
-            const int q0 = I.q0, rows = item_rows(I), take = I.take;
+            const int q0 = I.q0, rows = item_rows(I);
             auto load_q = [&]() {
                 if (lane == 0) {
                     mbar_arrive_expect_tx(q_full, S::kQBytes);
@@ -482,7 +489,6 @@ attn_cached_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                 if (!wait(q_empty, (it - 1) & 1)) break;
                 load_q();
             }
-            i += take;
             ip.next();
         }
         if (queries > 0 && !warp_wait_far(q_full, (queries - 1) & 1, nullptr) && lane == 0)
@@ -492,8 +498,9 @@ attn_cached_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         TcPlace<4> wp;
         int i = 0;
         bool ok = true;
-        for (int it = 0; ok && i < steps; ++it) {
+        for (int it = 0; ok; ++it) {
             ok = wait(&item_full[ip.s], ip.phase);
+            if (!ok || items[ip.s].take == 0) break;
             // (a tree's window is as wide as its tree is deep)
             if (ok && !chain) ok = wait(&tab_full[it & 1], (it >> 1) & 1);
             if (!ok) break;
@@ -528,8 +535,10 @@ attn_cached_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
             TcPlace<NK> kp;
             bool ok = true;
             int i = 0;
-            for (int it = 0; ok && i < steps; ++it) {
-                ok = one(&item_full[ip.s], ip.phase) && one(q_full, it & 1);
+            for (int it = 0; ok; ++it) {
+                ok = one(&item_full[ip.s], ip.phase);
+                if (!ok || items[ip.s].take == 0) break;
+                ok = one(q_full, it & 1);
                 if (!ok) break;
                 const int take = items[ip.s].take;
                 const uint32_t idesc =
@@ -566,9 +575,10 @@ attn_cached_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
             TcPlace<NV> vp;
             int i = 0, tail = 0;
             bool ok = true;
-            for (int it = 0; ok && i < steps; ++it) {
-                ok = one(&item_full[ip.s], ip.phase) &&
-                     (it < 2 || one(&o_empty[it & 1], (it / 2 - 1) & 1));
+            for (int it = 0; ok; ++it) {
+                ok = one(&item_full[ip.s], ip.phase);
+                if (!ok || items[ip.s].take == 0) break;
+                ok = it < 2 || one(&o_empty[it & 1], (it / 2 - 1) & 1);
                 if (!ok) break;
                 const TcItem& I = items[ip.s];
                 const int take = I.take, part0 = item_part0(I);
@@ -609,8 +619,10 @@ attn_cached_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         const int64_t lim = int64_t{1} << 30;
         int i = 0;                                      // first step of the item
         bool ok = true;
-        for (int it = 0; ok && i < steps; ++it) {
-            ok = wait(&item_full[ip.s], ip.phase) && wait(&tab_full[it & 1], (it >> 1) & 1);
+        for (int it = 0; ok; ++it) {
+            ok = wait(&item_full[ip.s], ip.phase);
+            if (!ok || items[ip.s].take == 0) break;
+            ok = wait(&tab_full[it & 1], (it >> 1) & 1);
             if (!ok) break;
             const TcItem I = items[ip.s];
             const TcTables<NQ>& T = tabs[it & 1];
@@ -758,8 +770,10 @@ attn_cached_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         const uint32_t o_col = tmem + 256 + (static_cast<uint32_t>(quarter * 32) << 16);
         int i = 0, tail = 0;
         bool ok = true;
-        for (int it = 0; ok && i < steps; ++it) {
-            ok = wait(&item_full[ip.s], ip.phase) && wait(&tab_full[it & 1], (it >> 1) & 1);
+        for (int it = 0; ok; ++it) {
+            ok = wait(&item_full[ip.s], ip.phase);
+            if (!ok || items[ip.s].take == 0) break;
+            ok = wait(&tab_full[it & 1], (it >> 1) & 1);
             if (!ok) break;
             const TcItem I = items[ip.s];
             TcTables<NQ>& T = tabs[it & 1];

@@ -65,7 +65,7 @@ hstu_status_t validate_cached(hstu_dtype_t dtype, const CachedArgs& c, int32_t p
 }
 
 // The join of parts, as a programmatic dependent of the attention launch.
-template <int V, typename TOut, int BLOCKS>
+template <int V, typename TOut, int BLOCKS, int E = 0>
 hstu_status_t launch_join(const CachedArgs& a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kJoinBlocks);
@@ -76,7 +76,7 @@ hstu_status_t launch_join(const CachedArgs& a, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_cached_join_kernel<V, TOut, BLOCKS>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_cached_join_kernel<V, TOut, BLOCKS, E>, a);
     return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }
 
@@ -160,7 +160,7 @@ hstu_status_t launch_cached_tc(const CachedArgs& a, cudaStream_t stream) {
     if (!ensure_smem(attn_cached_tc_kernel<D, NQ>, S::kAlloc, done)) return HSTU_ERR_CUDA;
     attn_cached_tc_kernel<D, NQ><<<kMmaBlocks, kTcThreads, S::kAlloc, stream>>>(tq, tk, tv, a);
     const hstu_status_t st = launch_status();
-    return st == HSTU_OK ? launch_join<4, __nv_bfloat16, kMmaBlocks>(a, stream) : st;
+    return st == HSTU_OK ? launch_join<4, __nv_bfloat16, kMmaBlocks, kTcEnd>(a, stream) : st;
 }
 
 // Rows of a part: the most that an item of the kernels below can have.

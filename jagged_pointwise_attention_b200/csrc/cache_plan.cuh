@@ -213,9 +213,12 @@ __global__ void __launch_bounds__(kAppendWarps * 32) cache_append_kernel(const C
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int nk = a.k_bytes / static_cast<int>(sizeof(V));
     const int n = nk + a.v_bytes / static_cast<int>(sizeof(V));
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kAppendWarps + warp; t < a.T;
-         t += static_cast<int64_t>(gridDim.x) * kAppendWarps) {
-        const int64_t slot = a.slots[t];
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kAppendWarps;
+    int64_t t = static_cast<int64_t>(blockIdx.x) * kAppendWarps + warp;
+    int64_t ahead = t < a.T ? a.slots[t] : 0;   // the next token's slot
+    for (; t < a.T; t += stride) {
+        const int64_t slot = ahead;
+        if (t + stride < a.T) ahead = a.slots[t + stride];
         if (slot < 0 || slot >= a.num_slots) {
             if (slot >= 0 && lane == 0) raise_error(kErrBadInput);
             continue;           // a padded row: nothing to keep
