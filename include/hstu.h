@@ -416,8 +416,10 @@ hstu_status_t hstu_attn_bwd(hstu_dtype_t dtype, const void* q, int64_t q_stride,
  *
  * A step gives sequence b, which has ctx_lens[b] tokens in the cache (device
  * int32 [B]), the new tokens new_offsets[b] .. new_offsets[b+1]-1 of the
- * step's packed [total_new, ...] tensors (device int64 [B+1], from 0 to
- * total_new). They stand at positions ctx_lens[b], ctx_lens[b] + 1, ... of the
+ * step's packed [total_new, ...] tensors (device int64 [B+1], from 0 to at most
+ * total_new; rows behind the last sequence are padding, and a sequence may have
+ * no new tokens, so a captured graph can serve batches of any size up to its
+ * own). They stand at positions ctx_lens[b], ctx_lens[b] + 1, ... of the
  * cache. In order: hstu_cache_plan (which pages), hstu_cache_append (their keys
  * and values), hstu_attn_cached_fwd. */
 
@@ -427,8 +429,8 @@ hstu_status_t hstu_attn_bwd(hstu_dtype_t dtype, const void* q, int64_t q_stride,
  * sequence order from free_pages (device int32 [num_free]), starting at index
  * *free_start (device int32), and written to its row; *free_end (device int32)
  * gets the index of the first page not taken. slots (device int64 [total_new])
- * gets every new token's slot. Entries behind a sequence's last page are left
- * as they are. Where the list is short, the missing entries and the slots in
+ * gets every new token's slot, -1 for padded rows. Entries behind a sequence's
+ * last page are left as they are. Where the list is short, the missing entries and the slots in
  * them are -1 and *free_end is num_free; a sequence with impossible numbers
  * (negative lengths, more than max_pages pages, offsets that decrease) takes no
  * pages, its slots are -1; both report HSTU_ERR_BAD_INPUT. free_end must not
@@ -542,7 +544,8 @@ size_t hstu_layer_step_workspace_bytes(int64_t total_new, int32_t D, int32_t H, 
  * not read. w4_group 32, 64 or 128: W1 and W2 are codes [4 H d, D/2] and
  * [D, H d/2] with scales s1 [4 H d, D/group] and s2 [D, H d/group] as
  * hstu_quant_groups_w4 writes them, rows without gaps. Sizes as hstu_layer_fwd;
- * cache, batch and the rest as hstu_cache_append and hstu_attn_cached_fwd. */
+ * cache, batch and the rest as hstu_cache_append and hstu_attn_cached_fwd; rows
+ * of out behind the last sequence are not specified. */
 hstu_status_t hstu_layer_step_fwd(const void* x, int64_t total_new, int32_t D, const void* W1,
                                   const void* s1, const float* b1, const void* W2, const void* s2,
                                   const float* b2, int32_t w4_group, const float* ln_gamma,

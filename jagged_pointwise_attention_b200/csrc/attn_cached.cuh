@@ -164,7 +164,7 @@ struct Line {
         for (int b = b0; b < b1; ++b) {
             bool ok;
             const CachedSeq s = cached_seq(a, b, ok);
-            all_ok = all_ok && ok && (b > 0 || s.off == 0) && (b + 1 < a.B || a.off[a.B] == a.T);
+            all_ok = all_ok && ok && (b > 0 || s.off == 0);
             mine += per_head(s) * a.H;
         }
         if (report && !all_ok) raise_error(kErrBadInput);

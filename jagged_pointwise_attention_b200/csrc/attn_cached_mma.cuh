@@ -132,7 +132,7 @@ attn_cached_mma_kernel(const __grid_constant__ CUtensorMap tmK,
         at.j = 0;
         bool ok;
         at.s = cached_seq(a, at.b, ok);
-        ok = ok && (at.b > 0 || at.s.off == 0) && (at.b + 1 < a.B || a.off[a.B] == a.T);
+        ok = ok && (at.b > 0 || at.s.off == 0);
         if (!ok && at.h == 0 && at.qt == 0 && tid == 0) raise_error(kErrBadInput);
         left = at.qt * NQ < at.s.n ? L::tiles(at.s, at.qt) : 0;
         __syncthreads();

@@ -19,7 +19,7 @@ namespace hstu {
 
 struct CachePlanArgs {
     const int32_t* ctx;         // [B]
-    const int64_t* off;         // [B + 1], off[B] = T
+    const int64_t* off;         // [B + 1], off[B] <= T: the rows behind are padding
     int B;
     int64_t T;
     int shift;                  // log2(page_size)
@@ -49,7 +49,6 @@ __device__ __forceinline__ PlanSeq plan_seq(const CachePlanArgs& a, int b, bool&
     const int64_t o = a.off[b], e = a.off[b + 1];
     const int64_t c = a.ctx[b];
     ok = c >= 0 && o >= 0 && e >= o && e <= a.T && (b > 0 || o == 0) &&
-         (b + 1 < a.B || e == a.T) &&
          ((c + (e - o) + (1 << a.shift) - 1) >> a.shift) <= a.max_pages;
     s.off = o;
     s.ctx = ok ? static_cast<int>(c) : 0;
@@ -151,7 +150,9 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const CachePla
     }
 
     // slots of the block's tokens, part y
-    int64_t t0 = nb > 0 ? a.off[b0] : 0, t1 = nb > 0 ? a.off[b0 + nb] : 0;
+    // (the last block's go on to the end: padded rows get slot -1)
+    const int64_t end = a.off[a.B];
+    int64_t t0 = a.off[b0], t1 = last ? a.T : a.off[b0 + nb];
     t0 = t0 < 0 ? 0 : t0;
     t1 = t1 > a.T ? a.T : t1;
     const int page_mask = (1 << a.shift) - 1;
@@ -172,12 +173,12 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const CachePla
                                 : take(s_base[lo] + at - s_have[lo]);
             if (page >= 0) slot = (static_cast<int64_t>(page) << a.shift) | (p & page_mask);
         }
-        all_ok = all_ok && slot >= 0;
+        all_ok = all_ok && (slot >= 0 || t >= end);
         a.slots[t] = slot;
     }
     if (last && blockIdx.y == 0 && tid == 0) {
-        const int64_t end = start + before + mine;
-        a.free_end[0] = static_cast<int32_t>(end < a.num_free ? end : a.num_free);
+        const int64_t taken = start + before + mine;
+        a.free_end[0] = static_cast<int32_t>(taken < a.num_free ? taken : a.num_free);
     }
     if (!all_ok) raise_error(kErrBadInput);
 }

@@ -152,3 +152,41 @@ def test_random_batches(seed):
     ok()
     check_attn(s, a)
     assert torch.equal(a, call_attn(hstu, s))
+
+
+@pytest.mark.parametrize("d,most", [(32, 3), (64, 3), (64, 30), (128, 100)])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_padded_batches_and_shared_pages(d, most, dtype):
+    """Rows behind the last sequence and sequences without new tokens are
+    padding: no error, slots of -1, rows left as they were. Two sequences share
+    the pages of a common prefix."""
+    page, pad = 16, 9
+    s = make_step([700, 700, 0, 40], [most, 2, 0, 1], "tree", 2, d, d, page, dtype, seed=d + most)
+    s.table[1, : 640 // page] = s.table[0, : 640 // page]       # a common prefix of 640 tokens
+    T = s.T
+    q = torch.cat([s.q, torch.full((pad, 2, d), float("nan"), dtype=dtype)]).cuda()
+    ts = torch.from_numpy(np.concatenate([s.ts, np.zeros(pad, np.int64)])).cuda()
+    par = torch.from_numpy(np.concatenate([s.parents, np.full(pad, 77, np.int32)])).cuda()
+    out = torch.full((T + pad, 2, d), 4.0, dtype=dtype).cuda()
+    got = call_attn(hstu, s, q=q, timestamps=ts, parents=par, out=out)
+    ok()
+    check_attn(s, got[:T])
+    assert bool((out[T:] == 4.0).all())
+    # the plan and the append of the same batch
+    tab = torch.full((4, s.table.shape[1]), -1, dtype=torch.int32)
+    for b, c in enumerate(s.ctx):
+        tab[b, : -(-c // page)] = torch.from_numpy(s.table[b, : -(-c // page)])
+    tab = tab.cuda()
+    free = torch.arange(1000, 1100, dtype=torch.int32).cuda()
+    slots, end = hstu.hstu_cache_plan(torch.tensor(s.ctx, dtype=torch.int32).cuda(),
+                                      torch.from_numpy(s.off).cuda(), free,
+                                      torch.zeros(1, dtype=torch.int32).cuda(), tab, page, T + pad)
+    ok()
+    assert bool((slots[T:] == -1).all()) and bool((slots[:T] >= 0).all())
+    need = sum(-(-(c + n) // page) - -(-c // page) for c, n in zip(s.ctx, s.new))
+    assert end.item() == need
+    kc, vc = (torch.zeros(1100, page, 2, d, dtype=dtype).cuda() for _ in range(2))
+    ones = torch.ones_like(q)
+    hstu.hstu_cache_append(ones, ones, None, slots, kc, vc, None)
+    ok()
+    assert kc.float().sum().item() == T * 2 * d == vc.float().sum().item()

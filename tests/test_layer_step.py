@@ -187,3 +187,23 @@ def test_binding_refuses():
                  (with_(10, None), hstu.HstuError), (with_(4, srv.vc.transpose(1, 2)), ValueError)):
         with pytest.raises(e):
             hstu.hstu_layer_step_fwd(*a)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("group", [0, 64])
+def test_padded_batches(group):
+    """Rows behind the last sequence (not a number, times of zero) change no row
+    and raise no error."""
+    li = make_layer_inputs(5, lengths_override=[130, 1, 44])
+    W1, W2, o1, o2 = weights(li, group)
+    want = oracle.layer(li.seq_offsets, li.x, o1, o2, li.H, li.d, li.timestamps, li.pos_bias,
+                        li.time_bias, li.max_seqlen, ln_eps=li.ln_eps)
+    srv = Server(li, 16, 64, W1, W2)
+    off = li.seq_offsets
+    for new, pad in (([120, 0, 40], 3), ([4, 1, 0], 11), ([6, 0, 4], 1)):
+        rows = np.concatenate([np.arange(off[b] + srv.ctx[b], off[b] + srv.ctx[b] + n)
+                               for b, n in enumerate(new)]).astype(np.int64)
+        x = np.concatenate([li.x[rows], np.full((pad, li.x.shape[1]), np.nan, li.x.dtype)])
+        ts = np.concatenate([li.timestamps[rows], np.zeros(pad, li.timestamps.dtype)])
+        got = srv.step(x, ts, new)
+        assert_bf16_close(got[:len(rows)], want[rows], "step %s" % (new,))
