@@ -430,10 +430,11 @@ hstu_status_t hstu_attn_bwd(hstu_dtype_t dtype, const void* q, int64_t q_stride,
  * *free_start (device int32), and written to its row; *free_end (device int32)
  * gets the index of the first page not taken. slots (device int64 [total_new])
  * gets every new token's slot, -1 for padded rows. Entries behind a sequence's
- * last page are left as they are. Where the list is short, the missing entries and the slots in
- * them are -1 and *free_end is num_free; a sequence with impossible numbers
- * (negative lengths, more than max_pages pages, offsets that decrease) takes no
- * pages, its slots are -1; both report HSTU_ERR_BAD_INPUT. free_end must not
+ * last page are left as they are. Where the list is short, the missing entries
+ * and the slots in them are -1 and *free_end is num_free; a sequence with
+ * impossible numbers (negative lengths, more than max_pages pages, offsets that
+ * decrease) takes no pages, its slots are -1; both report HSTU_ERR_BAD_INPUT.
+ * free_end must not
  * be free_start. */
 hstu_status_t hstu_cache_plan(const int32_t* ctx_lens, const int64_t* new_offsets, int32_t B,
                               int64_t total_new, int32_t page_size, const int32_t* free_pages,

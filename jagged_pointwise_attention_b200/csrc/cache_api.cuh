@@ -224,21 +224,26 @@ hstu_status_t launch_linear_w4_g(const LinearW4Args& a, int warps, cudaStream_t 
 }
 
 // Two row tiles of W a block where they still fill the device twice (x is read
-// half as often), else one; K split over at most eight warps.
+// half as often), else one; K split over at most eight warps. More than 32 rows
+// of x: blocks of 64 and two row tiles where K is long enough to hide their start
+// and their waves leave at most a third of the SMs idle (64 rows, us, that and
+// blocks of 32: 4096 x 4096 19.5 and 21.5, 2048 x 8192 23.0 and 25.5; but 512 x
+// 4096 9.7 and 7.2, 2048 x 6000 22.5 and 20.5, 8192 x 2048 31 and 19.5).
 hstu_status_t run_linear_w4(const LinearW4Args& a, cudaStream_t stream) {
     const int nkb = a.K / 128;
     const bool wide = a.N >= 2 * 148 * 32;
     const int most = wide ? 4 : 8, warps = nkb < most ? nkb : most;
+    const int64_t blocks = (static_cast<int64_t>(a.N) + 31) / 32 * ((a.M + 63) / 64);
+    const bool tall = a.M > 32 && nkb >= 8 && (blocks + 147) / 148 * 148 * 2 <= blocks * 3;
     if (a.M <= 8)
         return wide ? launch_linear_w4_g<2, 1>(a, warps, stream)
                     : launch_linear_w4_g<1, 1>(a, warps, stream);
     if (a.M <= 16)
         return wide ? launch_linear_w4_g<2, 2>(a, warps, stream)
                     : launch_linear_w4_g<1, 2>(a, warps, stream);
-    if (a.M <= 32)
-        return wide ? launch_linear_w4_g<2, 4>(a, warps, stream)
-                    : launch_linear_w4_g<1, 4>(a, warps, stream);
-    return launch_linear_w4_g<1, 8>(a, warps, stream);
+    if (tall) return launch_linear_w4_g<2, 8>(a, warps, stream);
+    return wide ? launch_linear_w4_g<2, 4>(a, warps, stream)
+                : launch_linear_w4_g<1, 4>(a, warps, stream);
 }
 
 // workspace of a layer step: [LayerNorm(x)][U|V|Q|K][attention][gated rows][attention's own]

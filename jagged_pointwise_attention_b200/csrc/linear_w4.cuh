@@ -53,7 +53,9 @@ __device__ __forceinline__ void w4_store(const LinearW4Args& a, int64_t m, int n
 // By then the bound is the unpacking: eleven operations for eight codes, seven
 // of them on the integer pipe at half rate, which is 0.55 busy over the launch.
 // Four row tiles a warp (29 us), two or eight warps a block (31 us), six stages
-// (36 us) and x not loaded ahead (33 us) were slower.
+// (36 us) and x not loaded ahead (33 us) were slower. 64 rows: 96 us, bound by
+// the products' own issue and x, which every row block reads (128 us with eight
+// row tiles of x and one of W, 110 with two blocks of four).
 constexpr int kW4Stages = 4;
 constexpr int kW4Pitch = 80;        // bytes of a row in the ring: 64 and 16 against bank conflicts
 
@@ -103,10 +105,13 @@ __global__ void __launch_bounds__(256) linear_w4_kernel(const LinearW4Args a) {
     for (int i = 0; i < 2 * MT; ++i)
         sr[i] = a.s + static_cast<int64_t>(min(n0 + 8 * i + g, a.N - 1)) * a.lds;
 
-    // x and the scales are loaded a block ahead (x while that costs few registers)
+    // the scales are loaded a block ahead; x too while that costs few registers,
+    // else 32 codes ahead (24 rows, 8192 x 2048: 19.5 -> 17.4 us; two row tiles and
+    // 32 rows lose an eighth by it)
     constexpr int GB = 128 / G;          // groups of a block
     constexpr bool kAhead = NT <= 2;
-    constexpr int kUnroll = MT == 1 && NT == 4 ? 1 : 4;     // (there 13 and 20 us at 4096 x 4096)
+    constexpr bool kStep = (MT == 1 && NT == 4) || (MT == 2 && NT == 8);
+    constexpr int kUnroll = kStep ? 1 : 4;      // (one row tile, 32 rows: 13 and 20 us at 4096 x 4096)
     uint4 xn[kAhead ? NT : 1][4];
     __nv_bfloat16 sn[2 * MT][GB];
     auto ahead = [&](int kb) {
@@ -124,6 +129,11 @@ __global__ void __launch_bounds__(256) linear_w4_kernel(const LinearW4Args a) {
         }
     };
     ahead(kb0);
+    uint4 xj[kStep ? NT : 1];
+    if (kStep && kb0 < kb1) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) xj[kStep ? n : 0] = ldg_nc_v4(xr[n] + kb0 * 128);
+    }
     float acc[MT][NT][4] = {};
 #pragma unroll kUnroll
     for (int kb = kb0; kb < kb1; ++kb) {
@@ -159,7 +169,9 @@ __global__ void __launch_bounds__(256) linear_w4_kernel(const LinearW4Args a) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const uint4 v = kAhead ? xc[kAhead ? n : 0][j]
-                                       : __ldg(reinterpret_cast<const uint4*>(xr[n] + kb * 128 + j * 32));
+                                : kStep ? xj[kStep ? n : 0] : ldg_nc_v4(xr[n] + kb * 128 + j * 32);
+                if (kStep && (j < 3 || kb + 1 < kb1))
+                    xj[kStep ? n : 0] = ldg_nc_v4(xr[n] + kb * 128 + (j + 1) * 32);
                 xb[n][0] = __byte_perm(v.x, v.z, 0x5410);
                 xb[n][1] = __byte_perm(v.x, v.z, 0x7632);
                 xb[n][2] = __byte_perm(v.y, v.w, 0x5410);

@@ -164,3 +164,17 @@ def test_quantized_projection_close_to_the_weights():
     tol = X @ half.T
     tol = tol + UBF * (np.abs(want) + tol) + 1e-3
     assert np.all(np.abs(y.double().cpu().numpy() - want) <= tol)
+
+
+@pytest.mark.parametrize("G", [32, 64, 128])
+@pytest.mark.parametrize("M,K,N", [(33, 1024, 3190), (64, 1152, 3190), (65, 1024, 1600), (130, 2176, 1070),
+                                   (40, 1024, 9490), (34, 256, 9490), (25, 256, 9490), (23, 1408, 300),
+                                   (47, 896, 3190)])
+def test_linear_many_rows(M, K, N, G):
+    """More rows of x than a block of 32 takes: blocks of 64, and several blocks."""
+    x, c, s, b, r = problem(M, K, N, G, M + K)
+    ep = ("none", "silu", "residual")[(M + G // 32) % 3]
+    y = hstu.hstu_linear_w4_fwd(x.cuda(), torch.from_numpy(c).cuda(), s.cuda(), b.cuda(), ep,
+                                r.cuda() if ep == "residual" else None)
+    ok()
+    check(y, x, c, s, G, b, r, ep)
