@@ -434,8 +434,7 @@ hstu_status_t hstu_attn_bwd(hstu_dtype_t dtype, const void* q, int64_t q_stride,
  * and the slots in them are -1 and *free_end is num_free; a sequence with
  * impossible numbers (negative lengths, more than max_pages pages, offsets that
  * decrease) takes no pages, its slots are -1; both report HSTU_ERR_BAD_INPUT.
- * free_end must not
- * be free_start. */
+ * free_end must not be free_start. */
 hstu_status_t hstu_cache_plan(const int32_t* ctx_lens, const int64_t* new_offsets, int32_t B,
                               int64_t total_new, int32_t page_size, const int32_t* free_pages,
                               int32_t num_free, const int32_t* free_start, int32_t* block_table,

@@ -53,9 +53,10 @@ __device__ __forceinline__ void w4_store(const LinearW4Args& a, int64_t m, int n
 // By then the bound is the unpacking: eleven operations for eight codes, seven
 // of them on the integer pipe at half rate, which is 0.55 busy over the launch.
 // Four row tiles a warp (29 us), two or eight warps a block (31 us), six stages
-// (36 us) and x not loaded ahead (33 us) were slower. 64 rows: 96 us, bound by
-// the products' own issue and x, which every row block reads (128 us with eight
-// row tiles of x and one of W, 110 with two blocks of four).
+// (36 us) and x not loaded ahead (33 us) were slower. 64 rows: 96 us; 255
+// registers leave eight warps an SM, which wait for x and for their own results
+// (issue slots 31%, tensor pipe 38%). One row tile of W there was 128 us, two
+// blocks of 32 rows 110.
 constexpr int kW4Stages = 4;
 constexpr int kW4Pitch = 80;        // bytes of a row in the ring: 64 and 16 against bank conflicts
 
