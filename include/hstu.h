@@ -429,12 +429,13 @@ hstu_status_t hstu_attn_bwd(hstu_dtype_t dtype, const void* q, int64_t q_stride,
  * sequence order from free_pages (device int32 [num_free]), starting at index
  * *free_start (device int32), and written to its row; *free_end (device int32)
  * gets the index of the first page not taken. slots (device int64 [total_new])
- * gets every new token's slot, -1 for padded rows. Entries behind a sequence's
- * last page are left as they are. Where the list is short, the missing entries
- * and the slots in them are -1 and *free_end is num_free; a sequence with
- * impossible numbers (negative lengths, more than max_pages pages, offsets that
- * decrease) takes no pages, its slots are -1; both report HSTU_ERR_BAD_INPUT.
- * free_end must not be free_start. */
+ * gets every new token's slot, -1 for rows that belong to no sequence (padding).
+ * Entries behind a sequence's last page are left as they are. Where the list is
+ * short, the missing entries and the slots in them are -1 and *free_end is
+ * num_free; a sequence with impossible numbers (negative lengths, more than
+ * max_pages pages, offsets outside 0..total_new, that decrease or lie below an
+ * earlier one, a first one that is not 0) takes no pages, its slots are -1; both
+ * report HSTU_ERR_BAD_INPUT. B >= 1. free_end must not be free_start. */
 hstu_status_t hstu_cache_plan(const int32_t* ctx_lens, const int64_t* new_offsets, int32_t B,
                               int64_t total_new, int32_t page_size, const int32_t* free_pages,
                               int32_t num_free, const int32_t* free_start, int32_t* block_table,

@@ -456,8 +456,8 @@ def hstu_cache_plan(ctx_lens: torch.Tensor, new_offsets: torch.Tensor, free_page
     """Block tables and slot maps of a serving step, on the GPU.
 
     ctx_lens: int32 [B], tokens each sequence has in the cache; new_offsets:
-    int64 [B+1], packed offsets of its new tokens (at most total_new; rows
-    behind the last sequence are padding and get slot -1);
+    int64 [B+1], packed offsets of its new tokens (at most total_new; rows that
+    belong to no sequence are padding and get slot -1), B >= 1;
     free_pages: int32 [F], free page numbers, of which the first free_start
     (int32 [1]) are taken. Writes the new entries of block_table (int32 [B,
     max_pages]) in place and returns (slots int64 [total_new], free_end int32

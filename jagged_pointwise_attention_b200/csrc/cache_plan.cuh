@@ -42,13 +42,16 @@ struct PlanSeq {
     int ctx, n, have, need;     // need: pages to take
 };
 
+constexpr int64_t kPlanNone = INT64_MIN;    // less than every offset
+
 // One sequence's numbers; a sequence that cannot be (negative lengths, offsets
-// outside [0, T], more pages than a table row has) takes no pages, `ok` false.
-__device__ __forceinline__ PlanSeq plan_seq(const CachePlanArgs& a, int b, bool& ok) {
+// outside [0, T], one below `top`, the greatest before it, more pages than a
+// table row has) takes no pages, `ok` false.
+__device__ __forceinline__ PlanSeq plan_seq(const CachePlanArgs& a, int b, int64_t top, bool& ok) {
     PlanSeq s;
     const int64_t o = a.off[b], e = a.off[b + 1];
     const int64_t c = a.ctx[b];
-    ok = c >= 0 && o >= 0 && e >= o && e <= a.T && (b > 0 || o == 0) &&
+    ok = c >= 0 && o >= 0 && o >= top && e >= o && e <= a.T && (b > 0 || o == 0) &&
          ((c + (e - o) + (1 << a.shift) - 1) >> a.shift) <= a.max_pages;
     s.off = o;
     s.ctx = ok ? static_cast<int>(c) : 0;
@@ -72,6 +75,29 @@ __device__ __forceinline__ int64_t plan_block_sum(int64_t v, int64_t* warp_sums)
     return t;
 }
 
+// Greatest v of the threads before this one (kPlanNone for the first); `all`:
+// of the whole block.
+__device__ __forceinline__ int64_t plan_max_before(int64_t v, int64_t* warp_max, int64_t& all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v = max(v, u);
+    }
+    __syncthreads();            // what was in warp_max has been read
+    if (lane == 31) warp_max[warp] = v;
+    __syncthreads();
+    int64_t before = __shfl_up_sync(0xffffffffu, v, 1);
+    if (lane == 0) before = kPlanNone;
+    all = kPlanNone;
+#pragma unroll
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+        if (w < warp) before = max(before, warp_max[w]);
+        all = max(all, warp_max[w]);
+    }
+    return before;
+}
+
 // Block (x, y): sequences x * S .. x * S + S - 1, part y of their pages and
 // tokens. Every block adds up the pages of all sequences before its own (a
 // few loads a thread for thousands of sequences), so one launch needs no
@@ -90,21 +116,43 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const CachePla
     const int64_t start = a.free_start[0];
     bool all_ok = start >= 0 && start <= a.num_free;
 
+    // the pages of the sequences before, this thread's sequence, and whether an
+    // offset falls anywhere up to the block's last sequence
+    bool ok = true, fall = false;
     int64_t before = 0;
     for (int b = tid; b < b0; b += kPlanThreads) {
-        bool ok;
-        before += plan_seq(a, b, ok).need;
+        before += plan_seq(a, b, kPlanNone, ok).need;
+        fall = fall || a.off[b + 1] < a.off[b];
+    }
+    PlanSeq s;
+    s.need = 0;
+    int64_t top = kPlanNone;    // greatest offset before this thread's sequence
+    if (tid < nb) {
+        s = plan_seq(a, b0 + tid, kPlanNone, ok);
+        fall = fall || a.off[b0 + tid + 1] < a.off[b0 + tid];
+    }
+    if (__syncthreads_or(fall)) {
+        // rare: once more, with the greatest offset before each sequence, so that
+        // no row belongs to two of them
+        const int per = (b0 + kPlanThreads - 1) / kPlanThreads;
+        const int c0 = min(tid * per, b0), c1 = min(c0 + per, b0);
+        int64_t m = kPlanNone, all, own;
+        for (int b = c0; b < c1; ++b) m = max(m, a.off[b]);
+        int64_t run = plan_max_before(m, warp_sums, all);
+        before = 0;
+        for (int b = c0; b < c1; ++b) {
+            before += plan_seq(a, b, run, ok).need;
+            run = max(run, a.off[b]);
+        }
+        top = max(all, plan_max_before(tid < nb ? a.off[b0 + tid] : kPlanNone, warp_sums, own));
+        if (tid < nb) s = plan_seq(a, b0 + tid, top, ok);
     }
     before = plan_block_sum(before, warp_sums);
 
     // this block's sequences: numbers and the scan of their pages
-    PlanSeq s;
-    s.need = 0;
     if (tid < nb) {
-        bool ok;
-        s = plan_seq(a, b0 + tid, ok);
         all_ok = all_ok && ok;
-        s_off[tid] = s.off;
+        s_off[tid] = max(top, s.off);
         s_ctx[tid] = s.ctx;
         s_n[tid] = s.n;
         s_have[tid] = s.have;
@@ -149,10 +197,11 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const CachePla
         a.table[static_cast<int64_t>(b0 + lo) * a.table_stride + s_have[lo] + k] = page;
     }
 
-    // slots of the block's tokens, part y
-    // (the last block's go on to the end: padded rows get slot -1)
+    // slots of the block's rows, part y: from its first offset (row 0 in the
+    // first block) to the next block's (the end in the last): rows that belong to
+    // no sequence get slot -1
     const int64_t end = a.off[a.B];
-    int64_t t0 = a.off[b0], t1 = last ? a.T : a.off[b0 + nb];
+    int64_t t0 = b0 == 0 ? 0 : s_off[0], t1 = last ? a.T : max(s_off[nb - 1], a.off[b0 + nb]);
     t0 = t0 < 0 ? 0 : t0;
     t1 = t1 > a.T ? a.T : t1;
     const int page_mask = (1 << a.shift) - 1;

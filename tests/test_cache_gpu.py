@@ -232,3 +232,73 @@ def test_steps_together(dtype, H, d, page):
         elif kind == "chain":
             ctx = [c + n for c, n in zip(ctx, new)]
     ok()
+
+
+def plan_any_offsets(ctx, off, total, page, free, start, table):
+    """(table, slots, free_end, possible) for any offsets: a sequence is possible
+    when its lengths are not negative, its offsets lie in [0, total], begin at 0
+    for the first, and no earlier offset is greater than its own."""
+    table, slots, at, possible = table.copy(), np.full(total, -1, dtype=np.int64), start, []
+    top = np.maximum.accumulate(off)
+    for b in range(len(ctx)):
+        o, e = int(off[b]), int(off[b + 1])
+        fits = (ctx[b] >= 0 and 0 <= o <= e <= total and o >= top[b] and (b > 0 or o == 0)
+                and -(-(ctx[b] + e - o) // page) <= table.shape[1])
+        possible.append(bool(fits))
+        if not fits:
+            continue
+        have, end = -(-ctx[b] // page), -(-(ctx[b] + e - o) // page)
+        for k in range(have, end):
+            table[b, k] = free[at] if at < len(free) else -1
+            at += 1
+        for i in range(e - o):
+            g = int(table[b, (ctx[b] + i) // page])
+            slots[o + i] = g * page + (ctx[b] + i) % page if g >= 0 else -1
+    return table, slots, min(at, len(free)), possible
+
+
+def fallen_offsets(B, T, falls, seed):
+    rng = np.random.default_rng(seed)
+    off = np.concatenate([[0], np.sort(rng.integers(0, T + 1, B - 1)), [T]]).astype(np.int64)
+    for b in rng.choice(np.arange(1, B), falls, replace=False):
+        off[b] = rng.integers(-3, T + 4)
+    return off
+
+
+BAD_OFFSETS = [
+    ([3, 8, 10], 10), ([-2, 3, 10], 10), ([0, -3, 5, 9], 9), ([0, 10, 4, 12, 20], 20),
+    ([0, 4, 50, 12, 20], 20), ([7, 7], 7), ([5, 2], 6), ([0, 700, 300, 5000], 6000),
+    ([9, 700, 4000], 4500),
+    (fallen_offsets(290, 900, 5, 1), 900), (fallen_offsets(2500, 9000, 9, 2), 9000),
+    (fallen_offsets(80000, 100000, 40, 3), 100000),
+]
+
+
+@pytest.mark.parametrize("off,total", BAD_OFFSETS, ids=[str(i) for i in range(len(BAD_OFFSETS))])
+def test_plan_offsets_that_cannot_be(off, total):
+    """Offsets that do not begin at 0, fall, or lie outside the rows: no row keeps
+    what it held, none belongs to two sequences, the same result every time."""
+    off, page = np.asarray(off, dtype=np.int64), 16
+    B = len(off) - 1
+    rng = np.random.default_rng(B)
+    ctx = rng.integers(0, 40, B).astype(np.int32)
+    have = -(-ctx // page)
+    width = min(int((ctx.max() + np.abs(np.diff(off)).max()) // page + 2), 64)
+    table = np.full((B, width), -99, dtype=np.int32)
+    pool = rng.permutation(int(have.sum()) + B + total + 20).astype(np.int32)
+    at = np.concatenate([[0], np.cumsum(have)])
+    for b in range(B):
+        table[b, : have[b]] = pool[at[b]: at[b + 1]]
+    free = pool[at[B]:]
+    wt, ws, we, possible = plan_any_offsets(ctx.tolist(), off, total, page, free, 2, table)
+    assert not all(possible)
+    for _ in range(3):
+        t = torch.from_numpy(table).cuda()
+        slots = torch.arange(total).cuda()                      # numbers that would do as slots
+        _, end = hstu.hstu_cache_plan(
+            torch.from_numpy(ctx).cuda(), torch.from_numpy(off).cuda(), torch.from_numpy(free).cuda(),
+            torch.tensor([2], dtype=torch.int32).cuda(), t, page, total, slots=slots)
+        assert hstu.hstu_device_status() == _native.HSTU_ERR_BAD_INPUT
+        assert np.array_equal(slots.cpu().numpy(), ws)
+        assert np.array_equal(t.cpu().numpy(), wt)
+        assert end.item() == we
