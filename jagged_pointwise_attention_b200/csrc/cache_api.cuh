@@ -246,6 +246,149 @@ hstu_status_t run_linear_w4(const LinearW4Args& a, cudaStream_t stream) {
                 : launch_linear_w4_g<1, 4>(a, warps, stream);
 }
 
+// Each of the calls below is in two parts, what it refuses and what it launches,
+// so that the layer step refuses all its parts' arguments before the first launch.
+
+// Checks an append (nothing to do where total_new is 0) and lays out its
+// arguments; `mix`: every address and length in bytes, or-ed.
+hstu_status_t make_append(hstu_dtype_t dtype, const void* k, int64_t k_stride, const void* v,
+                          int64_t v_stride, const int64_t* timestamps, const int64_t* slots,
+                          int64_t total_new, int32_t H, int32_t d_qk, int32_t d_v, void* k_cache,
+                          int64_t k_page_stride, int64_t k_tok_stride, void* v_cache,
+                          int64_t v_page_stride, int64_t v_tok_stride, int64_t* ts_cache,
+                          int64_t ts_page_stride, int32_t num_pages, int32_t page_size,
+                          CacheAppendArgs& a, uint64_t& mix) {
+    if (dtype != HSTU_DTYPE_F32 && dtype != HSTU_DTYPE_BF16) return HSTU_ERR_INVALID_ARG;
+    if (total_new < 0 || H < 1 || d_qk < 1 || d_v < 1) return HSTU_ERR_INVALID_ARG;
+    const int shift = page_shift(page_size);
+    if (shift < 0) return HSTU_ERR_UNSUPPORTED;
+    if (!cache_size_ok(num_pages, page_size)) return HSTU_ERR_INVALID_ARG;
+    const int64_t rk = static_cast<int64_t>(H) * d_qk, rv = static_cast<int64_t>(H) * d_v;
+    if (rk > (1 << 28) || rv > (1 << 28)) return HSTU_ERR_UNSUPPORTED;
+    if (k_tok_stride < rk || v_tok_stride < rv ||
+        k_page_stride < (page_size - 1) * k_tok_stride + rk ||
+        v_page_stride < (page_size - 1) * v_tok_stride + rv)
+        return HSTU_ERR_INVALID_ARG;
+    if ((timestamps == nullptr) != (ts_cache == nullptr)) return HSTU_ERR_INVALID_ARG;
+    if (ts_cache && (ts_page_stride < page_size || reinterpret_cast<uintptr_t>(ts_cache) % 8))
+        return HSTU_ERR_INVALID_ARG;
+    if (total_new == 0) return HSTU_OK;
+    if (!k || !v || !slots || !k_cache || !v_cache) return HSTU_ERR_INVALID_ARG;
+    if (total_new > 1 && (k_stride < rk || v_stride < rv)) return HSTU_ERR_INVALID_ARG;
+    const int e = dtype == HSTU_DTYPE_BF16 ? 2 : 4;
+    a = {static_cast<const uint8_t*>(k), static_cast<const uint8_t*>(v), k_stride * e, v_stride * e,
+         static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), k_page_stride * e,
+         k_tok_stride * e, v_page_stride * e, v_tok_stride * e, static_cast<int>(rk * e),
+         static_cast<int>(rv * e), timestamps, ts_cache, ts_page_stride, slots, total_new,
+         static_cast<int64_t>(num_pages) * page_size, shift};
+    mix = reinterpret_cast<uint64_t>(k) | reinterpret_cast<uint64_t>(v) |
+          reinterpret_cast<uint64_t>(k_cache) | reinterpret_cast<uint64_t>(v_cache) | a.k_stride |
+          a.v_stride | a.kc_page | a.kc_tok | a.vc_page | a.vc_tok | a.k_bytes | a.v_bytes;
+    return mix % e ? HSTU_ERR_INVALID_ARG : HSTU_OK;
+}
+
+hstu_status_t launch_append(const CacheAppendArgs& a, uint64_t mix, cudaStream_t s) {
+    const int64_t blocks = (a.T + kAppendWarps - 1) / kAppendWarps;
+    const unsigned grid = static_cast<unsigned>(blocks < 8 * 148 ? blocks : 8 * 148);
+    if (mix % 16 == 0) cache_append_kernel<uint4><<<grid, kAppendWarps * 32, 0, s>>>(a);
+    else if (mix % 4 == 0) cache_append_kernel<uint32_t><<<grid, kAppendWarps * 32, 0, s>>>(a);
+    else cache_append_kernel<uint16_t><<<grid, kAppendWarps * 32, 0, s>>>(a);
+    return launch_status();
+}
+
+// Checks a call of the attention (nothing to do without sequences or new tokens)
+// and lays out its arguments.
+hstu_status_t make_cached(hstu_dtype_t dtype, const void* q, int64_t q_tok_stride, const void* k_cache,
+                          int64_t k_page_stride, int64_t k_tok_stride, const void* v_cache,
+                          int64_t v_page_stride, int64_t v_tok_stride, const int64_t* ts_cache,
+                          int64_t ts_page_stride, int32_t num_pages, int32_t page_size,
+                          const int32_t* block_table, int64_t table_stride, int32_t max_pages,
+                          const int32_t* ctx_lens, const int64_t* new_offsets, int32_t B,
+                          int64_t total_new, int32_t max_new, int32_t H, int32_t d_qk, int32_t d_v,
+                          const int64_t* timestamps, const int32_t* parents, const float* pos_bias,
+                          int32_t num_pos, const float* time_bias, int32_t num_time_buckets,
+                          int32_t max_seqlen, void* out, int64_t out_tok_stride, void* workspace,
+                          size_t workspace_bytes, CachedArgs& a) {
+    const bool use_time = ts_cache && timestamps && time_bias;
+    a = CachedArgs{};
+    a.q = q;
+    a.q_stride = q_tok_stride;
+    a.ts = use_time ? timestamps : nullptr;
+    a.parents = parents;
+    a.out = out;
+    a.out_stride = out_tok_stride;
+    a.k = k_cache;
+    a.v = v_cache;
+    a.k_page = k_page_stride;
+    a.k_tok = k_tok_stride;
+    a.v_page = v_page_stride;
+    a.v_tok = v_tok_stride;
+    a.tsc = use_time ? ts_cache : nullptr;
+    a.tsc_page = ts_page_stride;
+    a.num_pages = num_pages;
+    a.shift = page_shift(page_size);
+    a.table = block_table;
+    a.table_stride = table_stride;
+    a.max_pages = max_pages;
+    a.ctx = ctx_lens;
+    a.off = new_offsets;
+    a.B = B;
+    a.T = total_new;
+    a.max_new = max_new;
+    a.max_seqlen = max_seqlen;
+    a.H = H;
+    a.dqk = d_qk;
+    a.dv = d_v;
+    a.pos = pos_bias;
+    a.P = num_pos;
+    a.tb = use_time ? time_bias : nullptr;
+    a.NB = num_time_buckets;
+    a.inv_n = 1.0f / static_cast<float>(max_seqlen);
+    a.heads = static_cast<PartHead*>(workspace);
+    a.parts = reinterpret_cast<float*>(a.heads + (dtype == HSTU_DTYPE_F32 ? kSimtBlocks : kMmaBlocks));
+    a.part_rows = cached_part_rows(dtype, max_new, d_v);
+    return validate_cached(dtype, a, page_size, workspace, workspace_bytes,
+                           hstu_attn_cached_workspace_bytes(dtype, max_new, d_v));
+}
+
+hstu_status_t launch_cached(hstu_dtype_t dtype, const CachedArgs& a, cudaStream_t s) {
+    if (dtype == HSTU_DTYPE_BF16) {
+        if (a.dqk == 32) return run_cached_bf16<32>(a, s);
+        if (a.dqk == 64) return run_cached_bf16<64>(a, s);
+        return run_cached_bf16<128>(a, s);
+    }
+    const bool vec = aligned16(a.k) && aligned16(a.v) && a.k_page % 4 == 0 && a.k_tok % 4 == 0 &&
+                     a.v_page % 4 == 0 && a.v_tok % 4 == 0 && a.dqk % 4 == 0 && a.dv % 4 == 0;
+    return vec ? run_cached_simt<true>(a, s) : run_cached_simt<false>(a, s);
+}
+
+// Checks a 4-bit projection (nothing to do where M is 0) and lays out its arguments.
+hstu_status_t make_linear_w4(const void* x, int64_t ldx, int64_t M, int32_t K, const void* codes,
+                             int64_t ldc, const void* scales, int64_t lds, int32_t group, int32_t N,
+                             const float* bias, hstu_epilogue_t epilogue, const void* residual,
+                             int64_t ldr, void* y, int64_t ldy, LinearW4Args& a) {
+    if (M < 0 || K < 1 || N < 1) return HSTU_ERR_INVALID_ARG;
+    if (epilogue != HSTU_EPI_NONE && epilogue != HSTU_EPI_SILU && epilogue != HSTU_EPI_RESIDUAL)
+        return HSTU_ERR_INVALID_ARG;
+    if ((group != 32 && group != 64 && group != 128) || K % 128 || M > 65535 * 8 || N > 0x7fffffff - 64)
+        return HSTU_ERR_UNSUPPORTED;
+    if (M == 0) return HSTU_OK;
+    if (!x || !codes || !scales || !y || (epilogue == HSTU_EPI_RESIDUAL && !residual))
+        return HSTU_ERR_INVALID_ARG;
+    if (ldx < K || ldc < K / 2 || lds < K / group || ldy < N ||
+        (epilogue == HSTU_EPI_RESIDUAL && ldr < N))
+        return HSTU_ERR_INVALID_ARG;
+    if (!aligned16(x) || ldx % 8 || !aligned16(codes) || ldc % 16) return HSTU_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(scales) % 2 || reinterpret_cast<uintptr_t>(y) % 2 ||
+        reinterpret_cast<uintptr_t>(residual) % 2 || reinterpret_cast<uintptr_t>(bias) % 4)
+        return HSTU_ERR_INVALID_ARG;
+    a = {static_cast<const __nv_bfloat16*>(x), ldx, static_cast<int>(M), K, N, group,
+         static_cast<const uint8_t*>(codes), ldc, static_cast<const __nv_bfloat16*>(scales), lds, bias,
+         static_cast<const __nv_bfloat16*>(residual), ldr, static_cast<__nv_bfloat16*>(y), ldy,
+         static_cast<int>(epilogue)};
+    return HSTU_OK;
+}
+
 // workspace of a layer step: [LayerNorm(x)][U|V|Q|K][attention][gated rows][attention's own]
 struct LayerStepWs {
     size_t xn, uvqk, attn, y, own, total;
@@ -305,42 +448,13 @@ hstu_status_t hstu_cache_append(hstu_dtype_t dtype, const void* k, int64_t k_str
                                 void* v_cache, int64_t v_page_stride, int64_t v_tok_stride,
                                 int64_t* ts_cache, int64_t ts_page_stride, int32_t num_pages,
                                 int32_t page_size, void* stream) {
-    if (dtype != HSTU_DTYPE_F32 && dtype != HSTU_DTYPE_BF16) return HSTU_ERR_INVALID_ARG;
-    if (total_new < 0 || H < 1 || d_qk < 1 || d_v < 1) return HSTU_ERR_INVALID_ARG;
-    const int shift = page_shift(page_size);
-    if (shift < 0) return HSTU_ERR_UNSUPPORTED;
-    if (!cache_size_ok(num_pages, page_size)) return HSTU_ERR_INVALID_ARG;
-    const int64_t rk = static_cast<int64_t>(H) * d_qk, rv = static_cast<int64_t>(H) * d_v;
-    if (rk > (1 << 28) || rv > (1 << 28)) return HSTU_ERR_UNSUPPORTED;
-    if (k_tok_stride < rk || v_tok_stride < rv ||
-        k_page_stride < (page_size - 1) * k_tok_stride + rk ||
-        v_page_stride < (page_size - 1) * v_tok_stride + rv)
-        return HSTU_ERR_INVALID_ARG;
-    if ((timestamps == nullptr) != (ts_cache == nullptr)) return HSTU_ERR_INVALID_ARG;
-    if (ts_cache && (ts_page_stride < page_size || reinterpret_cast<uintptr_t>(ts_cache) % 8))
-        return HSTU_ERR_INVALID_ARG;
-    if (total_new == 0) return HSTU_OK;
-    if (!k || !v || !slots || !k_cache || !v_cache) return HSTU_ERR_INVALID_ARG;
-    if (total_new > 1 && (k_stride < rk || v_stride < rv)) return HSTU_ERR_INVALID_ARG;
-    const int e = dtype == HSTU_DTYPE_BF16 ? 2 : 4;
-    CacheAppendArgs a{static_cast<const uint8_t*>(k), static_cast<const uint8_t*>(v), k_stride * e,
-                      v_stride * e, static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache),
-                      k_page_stride * e, k_tok_stride * e, v_page_stride * e, v_tok_stride * e,
-                      static_cast<int>(rk * e), static_cast<int>(rv * e), timestamps, ts_cache,
-                      ts_page_stride, slots, total_new,
-                      static_cast<int64_t>(num_pages) * page_size, shift};
-    const uint64_t mix = reinterpret_cast<uint64_t>(k) | reinterpret_cast<uint64_t>(v) |
-                         reinterpret_cast<uint64_t>(k_cache) | reinterpret_cast<uint64_t>(v_cache) |
-                         a.k_stride | a.v_stride | a.kc_page | a.kc_tok | a.vc_page | a.vc_tok |
-                         a.k_bytes | a.v_bytes;
-    if (mix % e) return HSTU_ERR_INVALID_ARG;
-    const int64_t blocks = (total_new + kAppendWarps - 1) / kAppendWarps;
-    const unsigned grid = static_cast<unsigned>(blocks < 8 * 148 ? blocks : 8 * 148);
-    cudaStream_t s = as_stream(stream);
-    if (mix % 16 == 0) cache_append_kernel<uint4><<<grid, kAppendWarps * 32, 0, s>>>(a);
-    else if (mix % 4 == 0) cache_append_kernel<uint32_t><<<grid, kAppendWarps * 32, 0, s>>>(a);
-    else cache_append_kernel<uint16_t><<<grid, kAppendWarps * 32, 0, s>>>(a);
-    return launch_status();
+    CacheAppendArgs a;
+    uint64_t mix;
+    const hstu_status_t st = make_append(dtype, k, k_stride, v, v_stride, timestamps, slots, total_new, H,
+                                         d_qk, d_v, k_cache, k_page_stride, k_tok_stride, v_cache,
+                                         v_page_stride, v_tok_stride, ts_cache, ts_page_stride,
+                                         num_pages, page_size, a, mix);
+    return st != HSTU_OK || total_new == 0 ? st : launch_append(a, mix, as_stream(stream));
 }
 
 size_t hstu_attn_cached_workspace_bytes(hstu_dtype_t dtype, int32_t max_new, int32_t d_v) {
@@ -367,58 +481,14 @@ hstu_status_t hstu_attn_cached_fwd(hstu_dtype_t dtype, const void* q, int64_t q_
                                    int32_t num_time_buckets, int32_t max_seqlen, void* out,
                                    int64_t out_tok_stride, void* workspace, size_t workspace_bytes,
                                    void* stream) {
-    const bool use_time = ts_cache && timestamps && time_bias;
-    CachedArgs a{};
-    a.q = q;
-    a.q_stride = q_tok_stride;
-    a.ts = use_time ? timestamps : nullptr;
-    a.parents = parents;
-    a.out = out;
-    a.out_stride = out_tok_stride;
-    a.k = k_cache;
-    a.v = v_cache;
-    a.k_page = k_page_stride;
-    a.k_tok = k_tok_stride;
-    a.v_page = v_page_stride;
-    a.v_tok = v_tok_stride;
-    a.tsc = use_time ? ts_cache : nullptr;
-    a.tsc_page = ts_page_stride;
-    a.num_pages = num_pages;
-    a.shift = page_shift(page_size);
-    a.table = block_table;
-    a.table_stride = table_stride;
-    a.max_pages = max_pages;
-    a.ctx = ctx_lens;
-    a.off = new_offsets;
-    a.B = B;
-    a.T = total_new;
-    a.max_new = max_new;
-    a.max_seqlen = max_seqlen;
-    a.H = H;
-    a.dqk = d_qk;
-    a.dv = d_v;
-    a.pos = pos_bias;
-    a.P = num_pos;
-    a.tb = use_time ? time_bias : nullptr;
-    a.NB = num_time_buckets;
-    a.inv_n = 1.0f / static_cast<float>(max_seqlen);
-    a.heads = static_cast<PartHead*>(workspace);
-    a.parts = reinterpret_cast<float*>(a.heads + (dtype == HSTU_DTYPE_F32 ? kSimtBlocks : kMmaBlocks));
-    a.part_rows = cached_part_rows(dtype, max_new, d_v);
-    const hstu_status_t st =
-        validate_cached(dtype, a, page_size, workspace, workspace_bytes,
-                        hstu_attn_cached_workspace_bytes(dtype, max_new, d_v));
-    if (st != HSTU_OK || B == 0 || total_new == 0) return st;
-    if (dtype == HSTU_DTYPE_BF16) {
-        if (d_qk == 32) return run_cached_bf16<32>(a, as_stream(stream));
-        if (d_qk == 64) return run_cached_bf16<64>(a, as_stream(stream));
-        return run_cached_bf16<128>(a, as_stream(stream));
-    }
-    const bool vec = aligned16(k_cache) && aligned16(v_cache) && k_page_stride % 4 == 0 &&
-                     k_tok_stride % 4 == 0 && v_page_stride % 4 == 0 && v_tok_stride % 4 == 0 &&
-                     d_qk % 4 == 0 && d_v % 4 == 0;
-    return vec ? run_cached_simt<true>(a, as_stream(stream))
-               : run_cached_simt<false>(a, as_stream(stream));
+    CachedArgs a;
+    const hstu_status_t st = make_cached(
+        dtype, q, q_tok_stride, k_cache, k_page_stride, k_tok_stride, v_cache, v_page_stride,
+        v_tok_stride, ts_cache, ts_page_stride, num_pages, page_size, block_table, table_stride,
+        max_pages, ctx_lens, new_offsets, B, total_new, max_new, H, d_qk, d_v, timestamps, parents,
+        pos_bias, num_pos, time_bias, num_time_buckets, max_seqlen, out, out_tok_stride, workspace,
+        workspace_bytes, a);
+    return st != HSTU_OK || B == 0 || total_new == 0 ? st : launch_cached(dtype, a, as_stream(stream));
 }
 
 hstu_status_t hstu_quant_groups_w4(const void* W, int64_t ldw, int64_t N, int32_t K, int32_t group,
@@ -449,27 +519,10 @@ hstu_status_t hstu_linear_w4_fwd(const void* x, int64_t ldx, int64_t M, int32_t 
                                  int32_t N, const float* bias, hstu_epilogue_t epilogue,
                                  const void* residual, int64_t ldr, void* y, int64_t ldy,
                                  void* stream) {
-    if (M < 0 || K < 1 || N < 1) return HSTU_ERR_INVALID_ARG;
-    if (epilogue != HSTU_EPI_NONE && epilogue != HSTU_EPI_SILU && epilogue != HSTU_EPI_RESIDUAL)
-        return HSTU_ERR_INVALID_ARG;
-    if ((group != 32 && group != 64 && group != 128) || K % 128 || M > 65535 * 8 || N > 0x7fffffff - 64)
-        return HSTU_ERR_UNSUPPORTED;
-    if (M == 0) return HSTU_OK;
-    if (!x || !codes || !scales || !y || (epilogue == HSTU_EPI_RESIDUAL && !residual))
-        return HSTU_ERR_INVALID_ARG;
-    if (ldx < K || ldc < K / 2 || lds < K / group || ldy < N ||
-        (epilogue == HSTU_EPI_RESIDUAL && ldr < N))
-        return HSTU_ERR_INVALID_ARG;
-    if (!aligned16(x) || ldx % 8 || !aligned16(codes) || ldc % 16) return HSTU_ERR_INVALID_ARG;
-    if (reinterpret_cast<uintptr_t>(scales) % 2 || reinterpret_cast<uintptr_t>(y) % 2 ||
-        reinterpret_cast<uintptr_t>(residual) % 2 || reinterpret_cast<uintptr_t>(bias) % 4)
-        return HSTU_ERR_INVALID_ARG;
-    LinearW4Args a{static_cast<const __nv_bfloat16*>(x), ldx, static_cast<int>(M), K, N, group,
-                   static_cast<const uint8_t*>(codes), ldc,
-                   static_cast<const __nv_bfloat16*>(scales), lds, bias,
-                   static_cast<const __nv_bfloat16*>(residual), ldr,
-                   static_cast<__nv_bfloat16*>(y), ldy, static_cast<int>(epilogue)};
-    return run_linear_w4(a, as_stream(stream));
+    LinearW4Args a;
+    const hstu_status_t st = make_linear_w4(x, ldx, M, K, codes, ldc, scales, lds, group, N, bias,
+                                            epilogue, residual, ldr, y, ldy, a);
+    return st != HSTU_OK || M == 0 ? st : run_linear_w4(a, as_stream(stream));
 }
 
 size_t hstu_layer_step_workspace_bytes(int64_t total_new, int32_t D, int32_t H, int32_t d,
@@ -512,39 +565,51 @@ hstu_status_t hstu_layer_step_fwd(const void* x, int64_t total_new, int32_t D, c
     __nv_bfloat16* uvqk = reinterpret_cast<__nv_bfloat16*>(ws + w.uvqk);
     __nv_bfloat16* attn = reinterpret_cast<__nv_bfloat16*>(ws + w.attn);
     __nv_bfloat16* ygate = reinterpret_cast<__nv_bfloat16*>(ws + w.y);
-    auto project = [&](const void* a, int32_t K, const void* W, const void* sc, int32_t N,
-                       const float* b, hstu_epilogue_t epi, const void* r, void* y) {
-        if (w4_group)
-            return hstu_linear_w4_fwd(a, K, T, K, W, K / 2, sc, K / w4_group, w4_group, N, b, epi, r, N,
-                                      y, N, stream);
-        return run_linear(a, K, T, K, W, K, N, b, epi, r, N, y, N, s);
-    };
     // 1. [LayerNorm(x) ->] f1 with the SiLU epilogue
-    const void* xin = x;
-    hstu_status_t st = HSTU_OK;
-    if (input_norm) {
-        xin = ws + w.xn;
-        st = run_ln_gate_any(false, false, x, D, nullptr, 0, T, D, in_gamma, in_beta, ln_eps, ws + w.xn,
-                             D, nullptr, 0, nullptr, s);
-        if (st != HSTU_OK) return st;
-    }
-    st = project(xin, D, W1, s1, 4 * F, b1, HSTU_EPI_SILU, nullptr, uvqk);
-    if (st != HSTU_OK) return st;
     // 2. the new keys and values into the cache, then the attention over it
-    st = hstu_cache_append(HSTU_DTYPE_BF16, uvqk + 3 * F, 4 * F, uvqk + F, 4 * F, timestamps, slots, T, H,
-                           d, d, k_cache, k_page_stride, k_tok_stride, v_cache, v_page_stride,
-                           v_tok_stride, ts_cache, ts_page_stride, num_pages, page_size, stream);
-    if (st != HSTU_OK) return st;
-    st = hstu_attn_cached_fwd(HSTU_DTYPE_BF16, uvqk + 2 * F, 4 * F, k_cache, k_page_stride, k_tok_stride,
-                              v_cache, v_page_stride, v_tok_stride, ts_cache, ts_page_stride, num_pages,
-                              page_size, block_table, table_stride, max_pages, ctx_lens, new_offsets, B,
-                              T, max_new, H, d, d, timestamps, parents, pos_bias, num_pos, time_bias,
-                              num_time_buckets, max_seqlen, attn, F, ws + w.own, w.total - w.own, stream);
-    if (st != HSTU_OK) return st;
     // 3. gate, f2 with the residual
-    st = run_ln_gate(attn, F, uvqk, 4 * F, T, F, ln_gamma, ln_beta, ln_eps, ygate, F, s);
+    // All is checked before the first launch: a refused call leaves the cache as it was.
+    const void* xin = input_norm ? ws + w.xn : x;
+    CacheAppendArgs put;
+    CachedArgs att;
+    LinearW4Args f1, f2;
+    uint64_t mix;
+    hstu_status_t st = ln_eps >= 0.0f && aligned16(x) ? HSTU_OK : HSTU_ERR_INVALID_ARG;
+    if (st == HSTU_OK)
+        st = w4_group ? make_linear_w4(xin, D, T, D, W1, D / 2, s1, D / w4_group, w4_group, 4 * F, b1,
+                                       HSTU_EPI_SILU, nullptr, 0, uvqk, 4 * F, f1)
+                      : check_linear(false, xin, D, nullptr, T, D, W1, D, nullptr, 4 * F, HSTU_EPI_SILU,
+                                     nullptr, 0, uvqk, 4 * F);
+    if (st == HSTU_OK)
+        st = make_append(HSTU_DTYPE_BF16, uvqk + 3 * F, 4 * F, uvqk + F, 4 * F, timestamps, slots, T, H, d,
+                         d, k_cache, k_page_stride, k_tok_stride, v_cache, v_page_stride, v_tok_stride,
+                         ts_cache, ts_page_stride, num_pages, page_size, put, mix);
+    if (st == HSTU_OK)
+        st = make_cached(HSTU_DTYPE_BF16, uvqk + 2 * F, 4 * F, k_cache, k_page_stride, k_tok_stride, v_cache,
+                         v_page_stride, v_tok_stride, ts_cache, ts_page_stride, num_pages, page_size,
+                         block_table, table_stride, max_pages, ctx_lens, new_offsets, B, T, max_new, H, d,
+                         d, timestamps, parents, pos_bias, num_pos, time_bias, num_time_buckets,
+                         max_seqlen, attn, F, ws + w.own, w.total - w.own, att);
+    if (st == HSTU_OK)
+        st = w4_group ? make_linear_w4(ygate, F, T, F, W2, F / 2, s2, F / w4_group, w4_group, D, b2,
+                                       HSTU_EPI_RESIDUAL, x, D, out, D, f2)
+                      : check_linear(false, ygate, F, nullptr, T, F, W2, F, nullptr, D, HSTU_EPI_RESIDUAL,
+                                     x, D, out, D);
     if (st != HSTU_OK) return st;
-    return project(ygate, F, W2, s2, D, b2, HSTU_EPI_RESIDUAL, x, out);
+    if (input_norm)
+        st = run_ln_gate_any(false, false, x, D, nullptr, 0, T, D, in_gamma, in_beta, ln_eps, ws + w.xn, D,
+                             nullptr, 0, nullptr, s);
+    if (st == HSTU_OK)
+        st = w4_group ? run_linear_w4(f1, s)
+                      : run_linear(xin, D, T, D, W1, D, 4 * F, b1, HSTU_EPI_SILU, nullptr, 0, uvqk, 4 * F, s);
+    if (st == HSTU_OK) st = launch_append(put, mix, s);
+    if (st == HSTU_OK) st = launch_cached(HSTU_DTYPE_BF16, att, s);
+    if (st == HSTU_OK)
+        st = run_ln_gate(attn, F, uvqk, 4 * F, T, F, ln_gamma, ln_beta, ln_eps, ygate, F, s);
+    if (st == HSTU_OK)
+        st = w4_group ? run_linear_w4(f2, s)
+                      : run_linear(ygate, F, T, F, W2, F, D, b2, HSTU_EPI_RESIDUAL, x, D, out, D, s);
+    return st;
 }
 
 }  // extern "C"

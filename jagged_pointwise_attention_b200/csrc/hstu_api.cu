@@ -410,12 +410,10 @@ hstu_status_t launch_gemm(unsigned grid, cudaStream_t stream, const CUtensorMap&
     return launch_status();
 }
 
-// y = epilogue(x W^T [* sx sw] + b): bf16 operands, or E4M3 codes with
-// row scales (fp8)
-hstu_status_t run_linear_any(bool fp8, const void* x, int64_t ldx, const float* sx, int64_t M,
-                             int32_t K, const void* W, int64_t ldw, const float* sw, int32_t N,
-                             const float* bias, hstu_epilogue_t epi, const void* residual,
-                             int64_t ldr, void* y, int64_t ldy, cudaStream_t stream) {
+hstu_status_t check_linear(bool fp8, const void* x, int64_t ldx, const float* sx, int64_t M,
+                           int32_t K, const void* W, int64_t ldw, const float* sw, int32_t N,
+                           hstu_epilogue_t epi, const void* residual, int64_t ldr, const void* y,
+                           int64_t ldy) {
     if (M < 0 || K < 1 || N < 1) return HSTU_ERR_INVALID_ARG;
     if (epi != HSTU_EPI_NONE && epi != HSTU_EPI_SILU && epi != HSTU_EPI_RESIDUAL)
         return HSTU_ERR_INVALID_ARG;
@@ -429,6 +427,18 @@ hstu_status_t run_linear_any(bool fp8, const void* x, int64_t ldx, const float* 
     if (!aligned16(x) || !aligned16(W) || !aligned16(y)) return HSTU_ERR_INVALID_ARG;
     if (epi == HSTU_EPI_RESIDUAL && (!residual || ldr < N || ldr % 8 || !aligned16(residual)))
         return HSTU_ERR_INVALID_ARG;
+    return HSTU_OK;
+}
+
+// y = epilogue(x W^T [* sx sw] + b): bf16 operands, or E4M3 codes with
+// row scales (fp8)
+hstu_status_t run_linear_any(bool fp8, const void* x, int64_t ldx, const float* sx, int64_t M,
+                             int32_t K, const void* W, int64_t ldw, const float* sw, int32_t N,
+                             const float* bias, hstu_epilogue_t epi, const void* residual,
+                             int64_t ldr, void* y, int64_t ldy, cudaStream_t stream) {
+    const hstu_status_t st =
+        check_linear(fp8, x, ldx, sx, M, K, W, ldw, sw, N, epi, residual, ldr, y, ldy);
+    if (st != HSTU_OK || M == 0) return st;
     // 128 x 256 output tiles when N allows (fewer operand bytes per FLOP),
     // else 128 x 128
     const int bn = N % 256 == 0 ? 256 : 128;

@@ -207,3 +207,71 @@ def test_padded_batches(group):
         ts = np.concatenate([li.timestamps[rows], np.zeros(pad, li.timestamps.dtype)])
         got = srv.step(x, ts, new)
         assert_bf16_close(got[:len(rows)], want[rows], "step %s" % (new,))
+
+
+def test_every_refusal_comes_before_any_launch():
+    """Without a GPU a launch fails with a CUDA error: what the parts of the layer
+    refuse (the projections, the append, the attention) is refused first."""
+    build()
+    lib = _native.load()
+
+    def call(x=16, T=4, D=512, W1=16, s1=16, b1=None, W2=16, s2=16, b2=None, group=0, eps=1e-5, norm=0,
+             kc=16, kp=None, kt=None, vc=16, vp=None, vt=None, tsc=16, tsp=16, n=4, page=16, table=16,
+             tstride=8, maxp=8, ctx=16, off=16, B=2, slots=16, max_new=2, H=4, d=128, ts=16, par=None,
+             pos=16, P=8, tb=16, NB=8, N=64, out=16, ws=16):
+        row = H * d
+        kt, vt = row if kt is None else kt, row if vt is None else vt
+        kp, vp = 16 * kt if kp is None else kp, 16 * vt if vp is None else vp
+        return lib.hstu_layer_step_fwd(x, T, D, W1, s1, b1, W2, s2, b2, group, None, None, eps, norm, None,
+                                       None, kc, kp, kt, vc, vp, vt, tsc, tsp, n, page, table, tstride,
+                                       maxp, ctx, off, B, slots, max_new, H, d, ts, par, pos, P, tb, NB, N,
+                                       out, ws, 1 << 40, None)
+    for kw in (dict(N=0), dict(N=131073), dict(maxp=0), dict(tstride=7), dict(table=None), dict(ctx=None),
+               dict(off=None), dict(P=0), dict(NB=0), dict(NB=1025), dict(n=0), dict(n=1 << 28),
+               dict(kc=None), dict(vc=None), dict(kc=24), dict(vc=24), dict(kt=511), dict(kt=516),
+               dict(vt=516), dict(kp=16 * 512 - 1), dict(vp=16 * 512 - 8), dict(tsp=15), dict(tsc=20),
+               dict(x=24), dict(W1=24), dict(W2=24), dict(out=24), dict(eps=-1.0), dict(eps=float("nan")),
+               dict(group=64, W1=24), dict(group=64, W2=24), dict(group=64, s1=17), dict(group=64, s2=17),
+               dict(group=64, b1=18), dict(group=64, b2=18), dict(group=64, x=24),
+               dict(norm=1, eps=-1.0)):
+        assert call(**kw) == INV, kw
+    for kw in (dict(page=8), dict(page=24), dict(par=16, max_new=257), dict(group=64, T=65535 * 8 + 1)):
+        assert call(**kw) == UNS, kw
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("group", [0, 64])
+def test_a_refused_call_leaves_the_cache_and_the_output(group):
+    li = make_layer_inputs(5, lengths_override=[40])
+    W1, W2, _, _ = weights(li, group)
+    srv = Server(li, 16, 8, W1, W2)
+    srv.step(li.x[:30], li.timestamps[:30], [30])
+    pages = srv.table[0, :2].cpu().tolist()
+    pos, tb = srv.pos, srv.tb
+    wide = torch.zeros(li.H, 1025).cuda()
+    x = dev(li.x[30:32], BF)
+    odd = torch.zeros(x.numel() + 4, dtype=BF).cuda()[4:].view_as(x)
+    out = torch.full_like(x, 3.0)
+
+    def call(x=x, parents=None, tb=tb, N=64, max_new=2, out=out, eps=1e-5):
+        return hstu.hstu_layer_step_fwd(
+            x, W1, W2, srv.kc, srv.vc, srv.tsc, srv.table, torch.tensor([30], dtype=torch.int32).cuda(),
+            torch.tensor([0, 2]).cuda(), torch.tensor([pages[1] * 16 + 14, pages[1] * 16 + 15]).cuda(),
+            dev(li.timestamps[30:32]), parents, pos, tb, N, max_new, ln_eps=eps, out=out)
+    before = [t.clone() for t in (srv.kc, srv.vc, srv.tsc)]
+    none = torch.full((2,), -1, dtype=torch.int32).cuda()
+    refused = [dict(N=0), dict(N=131073), dict(tb=wide), dict(parents=none, max_new=257), dict(eps=-1.0),
+               dict(x=odd)]
+    if group == 0:                  # (the 4-bit projection writes rows of any alignment)
+        refused.append(dict(out=odd))
+    for kw in refused:
+        with pytest.raises(hstu.HstuError):
+            call(**kw)
+        torch.cuda.synchronize()
+        for t, b in zip((srv.kc, srv.vc, srv.tsc), before):
+            assert torch.equal(t.view(torch.int16 if t.dtype == BF else t.dtype),
+                               b.view(torch.int16 if b.dtype == BF else b.dtype)), kw
+        assert bool((out == 3.0).all())
+    call()
+    torch.cuda.synchronize()
+    assert hstu.hstu_device_status() == 0 and not torch.equal(srv.tsc, before[2])
