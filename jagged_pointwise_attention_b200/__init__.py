@@ -14,6 +14,7 @@ out_i = (1/max_seqlen) sum_j silu(s_ij) v_j.
 
 from __future__ import annotations
 
+import contextlib
 from typing import Optional
 
 import torch
@@ -89,6 +90,28 @@ def hstu_attn_workspace_bytes(B: int, total_tokens: int, max_seqlen: int, H: int
     then the run's bias tables (num_pos: the position table's length, or 1
     without a position term)."""
     return int(_lib().hstu_attn_workspace_bytes(B, total_tokens, max_seqlen, H, max(num_pos, 1)))
+
+
+@contextlib.contextmanager
+def _allocating(stream):
+    """Where a call on `stream` allocates. Another stream than the current one
+    gets memory of its own: a block of the current stream's may still be in use
+    there by queued work, although it was let go of. The current stream reads what
+    goes through the given function (the results), so they are not handed out
+    again before that is done."""
+    raw = None if stream is None else _stream(stream)
+    if raw == 1:                        # cudaStreamLegacy: the default stream by another name
+        raw = 0
+    now = None if raw is None else torch.cuda.current_stream()
+    if now is None or raw == now.cuda_stream:
+        yield lambda t: t
+        return
+
+    def result(t):
+        t.record_stream(now)
+        return t
+    with torch.cuda.stream(torch.cuda.ExternalStream(raw) if raw else torch.cuda.default_stream()):
+        yield result
 
 
 def _workspace(nbytes: int, device) -> torch.Tensor:
@@ -586,13 +609,11 @@ def hstu_layer_step_fwd(x: torch.Tensor, W1, W2, k_cache: torch.Tensor, v_cache:
         if t is not None and (t.dtype != torch.float32 or t.dim() != 2 or t.shape[0] != H
                               or not t.is_contiguous()):
             raise ValueError("bias tables must be contiguous float32 [H, entries]")
-    own = []
-    if out is None:
-        out = torch.empty_like(x)
-        own.append(out)
-    if workspace is None:
-        workspace = _workspace(hstu_layer_step_workspace_bytes(T, D, H, d, max_new), x.device)
-        own.append(workspace)
+    with _allocating(stream) as result:
+        if out is None:
+            out = result(torch.empty_like(x))
+        if workspace is None:
+            workspace = _workspace(hstu_layer_step_workspace_bytes(T, D, H, d, max_new), x.device)
     strides = [s for t in (k_cache, v_cache)
                for s in (t.stride(0) if n > 1 else page * t.stride(1), t.stride(1))]
     _native.check("hstu_layer_step_fwd", _lib().hstu_layer_step_fwd(
@@ -605,9 +626,4 @@ def hstu_layer_step_fwd(x: torch.Tensor, W1, W2, k_cache: torch.Tensor, v_cache:
         0 if pos_bias is None else pos_bias.shape[1], _ptr(time_bias),
         0 if time_bias is None else time_bias.shape[1], int(max_seqlen), _ptr(out),
         _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
-    if stream is not None:
-        # allocated here and used on a stream that may not be the current one
-        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
-        for t in own:
-            t.record_stream(s)
     return out

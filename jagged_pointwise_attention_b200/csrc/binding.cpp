@@ -12,6 +12,7 @@
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -80,30 +81,42 @@ class Args {
         if (x != static_cast<int32_t>(x)) value_error(std::string(what) + " is out of range");
         return static_cast<int32_t>(x);
     }
-    // the raw stream: the current one for None
+    // the raw stream: the current one for None. Comes after the tensors and before
+    // empty().
     void* stream(int i) {
-        given_ = v_[i] != Py_None;
-        raw_ = given_ ? reinterpret_cast<cudaStream_t>(integer(i))
-                      : c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev_)).stream();
+        const c10::cuda::CUDAStream now =
+            c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev_));
+        raw_ = now.stream();
+        if (v_[i] == Py_None) return raw_;
+        cudaStream_t given = reinterpret_cast<cudaStream_t>(integer(i));
+        if (given == cudaStreamLegacy) given = nullptr;     // the default stream by another name
+        other_ = given != raw_;
+        raw_ = given;
         return raw_;
     }
+    // Memory of the call's own stream: a block of the current stream's may still be
+    // in use there by work that is queued, whoever let go of it.
     at::Tensor empty(at::IntArrayRef shape, at::ScalarType dtype) {
+        c10::cuda::OptionalCUDAStreamGuard guard;
+        if (other_)
+            guard.reset_stream(
+                c10::cuda::getStreamFromExternal(raw_, static_cast<c10::DeviceIndex>(dev_)));
         return at::detail::empty_cuda(shape, dtype, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(dev_)),
                                       std::nullopt);
     }
-    // Allocated by this call, used on a stream that is not the current one: the
-    // allocator must not hand the memory out again before that use.
-    void used(const at::Tensor& t) {
-        if (!given_ || !t.defined() || t.numel() == 0) return;
+    // A result that the caller's current stream will read: the allocator must not
+    // hand it out again, once it is let go of, before that use.
+    void result(const at::Tensor& t) {
+        if (!other_ || !t.defined() || t.numel() == 0) return;
         c10::cuda::CUDACachingAllocator::recordStream(
             t.storage().data_ptr(),
-            c10::cuda::getStreamFromExternal(raw_, static_cast<c10::DeviceIndex>(dev_)));
+            c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev_)));
     }
 
   private:
     PyObject* const* v_;
     int dev_ = -1;
-    bool given_ = false;
+    bool other_ = false;         // a stream was given that is not the current one
     cudaStream_t raw_ = nullptr;
 };
 
@@ -207,6 +220,7 @@ PyObject* cache_plan(PyObject* const* v, Py_ssize_t n) {
     const int64_t stride = table_of(table, B);
     if (total < 0) value_error("total_new is negative");
     const at::Tensor *slots = a.maybe(7, "slots"), *end = a.maybe(8, "free_end");
+    void* s = a.stream(9);
     at::Tensor own_slots, own_end;
     if (slots) want_flat(*slots, at::kLong, "slots", total);
     else slots = &(own_slots = a.empty({total}, at::kLong));
@@ -216,14 +230,13 @@ PyObject* cache_plan(PyObject* const* v, Py_ssize_t n) {
     } else {
         end = &(own_end = a.empty({1}, at::kInt));
     }
-    void* s = a.stream(9);
     check("hstu_cache_plan",
           api.plan(data<int32_t>(&ctx), data<int64_t>(&off), static_cast<int32_t>(B), total,
                    a.int32(5, "page_size"), data<int32_t>(&free), small(free.numel(), "free_pages"),
                    data<int32_t>(&start), data<int32_t>(&table), stride,
                    static_cast<int32_t>(table.size(1)), data<int64_t>(slots), data<int32_t>(end), s));
-    a.used(own_slots);
-    a.used(own_end);
+    a.result(own_slots);
+    a.result(own_end);
     PyObject *x = py_tensor(*slots), *y = py_tensor(*end);
     PyObject* r = x && y ? PyTuple_Pack(2, x, y) : nullptr;
     Py_XDECREF(x);
@@ -291,6 +304,7 @@ PyObject* attn_cached(PyObject* const* v, Py_ssize_t n) {
     }
     const int64_t stride = table_of(table, B), qs = rows_of(q, "q", T, H, dqk);
     const int32_t max_seqlen = a.int32(11, "max_seqlen"), max_new = a.int32(12, "max_new");
+    void* s = a.stream(15);
     at::Tensor own_out, own_ws;
     if (out) {
         if (out->scalar_type() != q.scalar_type()) type_error("out must have q's dtype");
@@ -304,7 +318,6 @@ PyObject* attn_cached(PyObject* const* v, Py_ssize_t n) {
     } else if (!ws->is_contiguous()) {
         value_error("workspace must be contiguous");
     }
-    void* s = a.stream(15);
     check("hstu_attn_cached_fwd",
           api.attn(dt, q.data_ptr(), qs, kc.data_ptr(), ck.page, ck.tok, vc.data_ptr(), cv.page,
                    cv.tok, data<int64_t>(tsc), ts_page(tsc, pages, page), small(pages, "num_pages"),
@@ -315,8 +328,7 @@ PyObject* attn_cached(PyObject* const* v, Py_ssize_t n) {
                    pos ? small(pos->size(1), "num_pos") : 0, data<float>(tb),
                    tb ? small(tb->size(1), "num_time_buckets") : 0, max_seqlen, out->data_ptr(), os,
                    ws->data_ptr(), static_cast<size_t>(ws->nbytes()), s));
-    a.used(own_out);
-    a.used(own_ws);
+    a.result(own_out);
     return py_tensor(*out);
 }
 
@@ -337,13 +349,13 @@ PyObject* quant_w4(PyObject* const* v, Py_ssize_t n) {
     const int64_t N = W.size(0), K = W.size(1);
     const int32_t G = a.int32(1, "group");
     const int64_t ld = matrix(W, at::kBFloat16, "W", N, K);
+    void* s = a.stream(2);
     at::Tensor codes = a.empty({N, K / 2}, at::kByte);
     at::Tensor scales = a.empty({N, G > 0 ? K / G : 0}, at::kBFloat16);
-    void* s = a.stream(2);
     check("hstu_quant_groups_w4", api.quant(W.data_ptr(), ld, N, small(K, "K"), G, codes.data_ptr(),
                                             K / 2, scales.data_ptr(), scales.size(1), s));
-    a.used(codes);
-    a.used(scales);
+    a.result(codes);
+    a.result(scales);
     PyObject *x = py_tensor(codes), *y = py_tensor(scales);
     PyObject* r = x && y ? PyTuple_Pack(2, x, y) : nullptr;
     Py_XDECREF(x);
@@ -367,17 +379,17 @@ PyObject* linear_w4(PyObject* const* v, Py_ssize_t n) {
     if (bias) want_flat(*bias, at::kFloat, "bias", N);
     if (epi == HSTU_EPI_RESIDUAL && res == nullptr) value_error("the residual epilogue needs residual");
     const int64_t ldr = epi == HSTU_EPI_RESIDUAL ? matrix(*res, at::kBFloat16, "residual", M, N) : 0;
+    void* s = a.stream(7);
     at::Tensor own;
     if (out == nullptr) out = &(own = a.empty({M, N}, at::kBFloat16));
     const int64_t ldy = matrix(*out, at::kBFloat16, "out", M, N);
-    void* s = a.stream(7);
     check("hstu_linear_w4_fwd",
           api.linear(x.data_ptr(), ldx, M, small(K, "K"), codes.data_ptr(), ldc, scales.data_ptr(),
                      lds, static_cast<int32_t>(K / ng), small(N, "N"), data<float>(bias),
                      static_cast<hstu_epilogue_t>(epi),
                      epi == HSTU_EPI_RESIDUAL ? res->data_ptr() : nullptr, ldr, out->data_ptr(), ldy,
                      s));
-    a.used(own);
+    a.result(own);
     return py_tensor(*out);
 }
 
