@@ -174,12 +174,13 @@ def hstu_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_offsets
     Returns out [T, H, d_v] = (1/max_seqlen) sum_{j<=i} silu(s_ij) v_j.
     """
     T, H, _ = q.shape
-    if out is None:
-        out = torch.empty((T, H, v.shape[2]), dtype=q.dtype, device=q.device)
-    a = _attn_args(q, k, v, seq_offsets, timestamps, pos_bias, time_bias, max_seqlen, out)
-    if workspace is None and a["dtype"] == _native.HSTU_DTYPE_BF16:
-        workspace = _workspace(hstu_attn_workspace_bytes(a["B"], T, max_seqlen, a["H"], a["P"]),
-                               q.device)
+    with _allocating(stream) as result:
+        if out is None:
+            out = result(torch.empty((T, H, v.shape[2]), dtype=q.dtype, device=q.device))
+        a = _attn_args(q, k, v, seq_offsets, timestamps, pos_bias, time_bias, max_seqlen, out)
+        if workspace is None and a["dtype"] == _native.HSTU_DTYPE_BF16:
+            workspace = _workspace(
+                hstu_attn_workspace_bytes(a["B"], T, max_seqlen, a["H"], a["P"]), q.device)
     _native.check("hstu_attn_fwd", _lib().hstu_attn_fwd(
         a["dtype"], a["q"], a["qs"], a["k"], a["ks"], a["v"], a["vs"], a["off"], a["B"], a["T"],
         a["H"], a["dqk"], a["dv"], a["ts"], a["pos"], a["P"], a["tb"], a["NB"], a["N"], a["out"],
@@ -193,8 +194,9 @@ def hstu_debug_bias_indices(seq_offsets: torch.Tensor, timestamps: torch.Tensor,
     _on_cuda(seq_offsets, timestamps)
     n = torch.diff(seq_offsets.cpu())
     E = int((n * (n + 1) // 2).sum())
-    pos = torch.zeros(max(E, 1), dtype=torch.int32, device=seq_offsets.device)
-    bkt = torch.zeros(max(E, 1), dtype=torch.int32, device=seq_offsets.device)
+    with _allocating(stream) as result:
+        pos = result(torch.zeros(max(E, 1), dtype=torch.int32, device=seq_offsets.device))
+        bkt = result(torch.zeros(max(E, 1), dtype=torch.int32, device=seq_offsets.device))
     _native.check("hstu_debug_bias_indices", _lib().hstu_debug_bias_indices(
         _ptr(seq_offsets), seq_offsets.numel() - 1, timestamps.numel(), _ptr(timestamps),
         num_pos, num_buckets, _ptr(pos), _ptr(bkt), _stream(stream)))
@@ -216,7 +218,8 @@ def hstu_linear_fwd(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tenso
     epi = {"none": _native.HSTU_EPI_NONE, "silu": _native.HSTU_EPI_SILU,
            "residual": _native.HSTU_EPI_RESIDUAL}[epilogue]
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        with _allocating(stream) as result:
+            out = result(torch.empty((M, N), dtype=torch.bfloat16, device=x.device))
     for t in (x, W, out) + ((residual,) if residual is not None else ()):
         if t.dtype != torch.bfloat16 or t.stride(1) != 1:
             raise ValueError("x, W, residual, out must be bf16 with unit column stride")
@@ -233,8 +236,9 @@ def hstu_quant_rows_e4m3(x: torch.Tensor, stream=None):
     if x.dtype != torch.bfloat16 or x.stride(1) != 1:
         raise ValueError("x must be bf16 with unit column stride")
     M, K = x.shape
-    codes = torch.empty((M, K), dtype=torch.uint8, device=x.device)
-    scales = torch.empty(M, dtype=torch.float32, device=x.device)
+    with _allocating(stream) as result:
+        codes = result(torch.empty((M, K), dtype=torch.uint8, device=x.device))
+        scales = result(torch.empty(M, dtype=torch.float32, device=x.device))
     _native.check("hstu_quant_rows_e4m3", _lib().hstu_quant_rows_e4m3(
         _ptr(x), x.stride(0), M, K, _ptr(codes), codes.stride(0), _ptr(scales), _stream(stream)))
     return codes, scales
@@ -252,7 +256,8 @@ def hstu_linear_fp8_fwd(xq: torch.Tensor, x_scales: torch.Tensor, wq: torch.Tens
     epi = {"none": _native.HSTU_EPI_NONE, "silu": _native.HSTU_EPI_SILU,
            "residual": _native.HSTU_EPI_RESIDUAL}[epilogue]
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=xq.device)
+        with _allocating(stream) as result:
+            out = result(torch.empty((M, N), dtype=torch.bfloat16, device=xq.device))
     if xq.dtype != torch.uint8 or wq.dtype != torch.uint8 or xq.stride(1) != 1 or wq.stride(1) != 1:
         raise ValueError("xq, wq must be uint8 E4M3 codes with unit column stride")
     if x_scales.dtype != torch.float32 or w_scales.dtype != torch.float32:
@@ -271,7 +276,8 @@ def hstu_layernorm_gate_fwd(a: torch.Tensor, u: torch.Tensor, gamma=None, beta=N
     _on_cuda(a, u, gamma, beta, out)
     M, F = a.shape
     if out is None:
-        out = torch.empty((M, F), dtype=torch.bfloat16, device=a.device)
+        with _allocating(stream) as result:
+            out = result(torch.empty((M, F), dtype=torch.bfloat16, device=a.device))
     _native.check("hstu_layernorm_gate_fwd", _lib().hstu_layernorm_gate_fwd(
         _ptr(a), a.stride(0), _ptr(u), u.stride(0), M, F, _ptr(gamma), _ptr(beta), float(eps),
         _ptr(out), out.stride(0), _stream(stream)))
@@ -285,7 +291,8 @@ def hstu_layernorm_fwd(a: torch.Tensor, gamma=None, beta=None, eps: float = 1e-5
     _on_cuda(a, gamma, beta, out)
     M, F = a.shape
     if out is None:
-        out = torch.empty((M, F), dtype=torch.bfloat16, device=a.device)
+        with _allocating(stream) as result:
+            out = result(torch.empty((M, F), dtype=torch.bfloat16, device=a.device))
     _native.check("hstu_layernorm_fwd", _lib().hstu_layernorm_fwd(
         _ptr(a), a.stride(0), M, F, _ptr(gamma), _ptr(beta), float(eps), _ptr(out),
         out.stride(0), _stream(stream)))
@@ -298,8 +305,9 @@ def hstu_layernorm_fp8_fwd(a: torch.Tensor, gamma=None, beta=None, eps: float = 
     kernel: (codes uint8 [M, F], scales fp32 [M])."""
     _on_cuda(a, gamma, beta)
     M, F = a.shape
-    codes = torch.empty((M, F), dtype=torch.uint8, device=a.device)
-    scales = torch.empty(M, dtype=torch.float32, device=a.device)
+    with _allocating(stream) as result:
+        codes = result(torch.empty((M, F), dtype=torch.uint8, device=a.device))
+        scales = result(torch.empty(M, dtype=torch.float32, device=a.device))
     _native.check("hstu_layernorm_fp8_fwd", _lib().hstu_layernorm_fp8_fwd(
         _ptr(a), a.stride(0), M, F, _ptr(gamma), _ptr(beta), float(eps), _ptr(codes),
         codes.stride(0), _ptr(scales), _stream(stream)))
@@ -328,10 +336,11 @@ def hstu_layer_fwd(x: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor, seq_offs
     for t in (x, W1, W2):
         if t.dtype != torch.bfloat16 or not t.is_contiguous():
             raise ValueError("x, W1, W2 must be contiguous bf16")
-    if out is None:
-        out = torch.empty_like(x)
-    if workspace is None:
-        workspace = _workspace(hstu_layer_workspace_bytes(T, B, D, H, d, max_seqlen), x.device)
+    with _allocating(stream) as result:
+        if out is None:
+            out = result(torch.empty_like(x))
+        if workspace is None:
+            workspace = _workspace(hstu_layer_workspace_bytes(T, B, D, H, d, max_seqlen), x.device)
     _native.check("hstu_layer_fwd", _lib().hstu_layer_fwd(
         _ptr(x), T, D, _ptr(W1), _ptr(b1), _ptr(W2), _ptr(b2), _ptr(ln_gamma), _ptr(ln_beta),
         float(ln_eps), 1 if input_norm else 0, _ptr(in_gamma), _ptr(in_beta),
@@ -348,8 +357,9 @@ def hstu_layernorm_gate_fp8_fwd(a: torch.Tensor, u: torch.Tensor, gamma=None, be
     kernel: (codes uint8 [M, F], scales fp32 [M])."""
     _on_cuda(a, u, gamma, beta)
     M, F = a.shape
-    codes = torch.empty((M, F), dtype=torch.uint8, device=a.device)
-    scales = torch.empty(M, dtype=torch.float32, device=a.device)
+    with _allocating(stream) as result:
+        codes = result(torch.empty((M, F), dtype=torch.uint8, device=a.device))
+        scales = result(torch.empty(M, dtype=torch.float32, device=a.device))
     _native.check("hstu_layernorm_gate_fp8_fwd", _lib().hstu_layernorm_gate_fp8_fwd(
         _ptr(a), a.stride(0), _ptr(u), u.stride(0), M, F, _ptr(gamma), _ptr(beta), float(eps),
         _ptr(codes), codes.stride(0), _ptr(scales), _stream(stream)))
@@ -381,10 +391,11 @@ def hstu_layer_fp8_fwd(x: torch.Tensor, W1q: torch.Tensor, w1_scales: torch.Tens
     for t in (W1q, W2q):
         if t.dtype != torch.uint8 or not t.is_contiguous():
             raise ValueError("W1q, W2q must be contiguous uint8 E4M3 codes")
-    if out is None:
-        out = torch.empty_like(x)
-    if workspace is None:
-        workspace = _workspace(hstu_layer_fp8_workspace_bytes(T, B, D, H, d, max_seqlen), x.device)
+    with _allocating(stream) as result:
+        if out is None:
+            out = result(torch.empty_like(x))
+        if workspace is None:
+            workspace = _workspace(hstu_layer_fp8_workspace_bytes(T, B, D, H, d, max_seqlen), x.device)
     _native.check("hstu_layer_fp8_fwd", _lib().hstu_layer_fp8_fwd(
         _ptr(x), T, D, _ptr(W1q), _ptr(w1_scales), _ptr(b1), _ptr(W2q), _ptr(w2_scales), _ptr(b2),
         _ptr(ln_gamma), _ptr(ln_beta), float(ln_eps), 1 if input_norm else 0, _ptr(in_gamma),
@@ -416,15 +427,16 @@ def hstu_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, dout: torch
     T, H, d = q.shape
     B = seq_offsets.numel() - 1
     use_time = timestamps is not None and time_bias is not None
-    if out is None:
-        f32 = dict(dtype=torch.float32, device=q.device)
-        out = (torch.empty((T, H, d), **f32), torch.empty((T, H, d), **f32),
-               torch.empty((T, H, d), **f32),
-               None if pos_bias is None else torch.empty_like(pos_bias),
-               torch.empty_like(time_bias) if use_time else None)
+    with _allocating(stream) as result:
+        if out is None:
+            f32 = dict(dtype=torch.float32, device=q.device)
+            out = (result(torch.empty((T, H, d), **f32)), result(torch.empty((T, H, d), **f32)),
+                   result(torch.empty((T, H, d), **f32)),
+                   None if pos_bias is None else result(torch.empty_like(pos_bias)),
+                   result(torch.empty_like(time_bias)) if use_time else None)
+        if workspace is None:
+            workspace = _workspace(hstu_attn_bwd_workspace_bytes(B, T, max_seqlen), q.device)
     dq, dk, dv, dpos, dtime = out
-    if workspace is None:
-        workspace = _workspace(hstu_attn_bwd_workspace_bytes(B, T, max_seqlen), q.device)
     _native.check("hstu_attn_bwd", _lib().hstu_attn_bwd(
         _native.HSTU_DTYPE_BF16, _ptr(q), q.stride(0), _ptr(k), k.stride(0), _ptr(v), v.stride(0),
         _ptr(dout), dout.stride(0), _ptr(seq_offsets), B, T, H, d, _ptr(timestamps),
@@ -447,10 +459,11 @@ def hstu_attn_bwd_f32(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, dout: t
     T, H, dqk = q.shape
     dvd = v.shape[2]
     B = seq_offsets.numel() - 1
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    dpos = None if pos_bias is None else torch.empty_like(pos_bias)
     use_time = timestamps is not None and time_bias is not None
-    dtime = torch.empty_like(time_bias) if use_time else None
+    with _allocating(stream) as result:
+        dq, dk, dv = (result(torch.empty_like(t)) for t in (q, k, v))
+        dpos = None if pos_bias is None else result(torch.empty_like(pos_bias))
+        dtime = result(torch.empty_like(time_bias)) if use_time else None
     _native.check("hstu_attn_bwd_f32", _lib().hstu_attn_bwd_f32(
         _ptr(q), _ptr(k), _ptr(v), _ptr(dout), _ptr(seq_offsets), B, T, H, dqk, dvd,
         _ptr(timestamps), _ptr(pos_bias), 0 if pos_bias is None else pos_bias.shape[1],

@@ -7,8 +7,8 @@ import pytest
 import torch
 
 import jagged_pointwise_attention_b200 as hstu
-from gen import make_layer_inputs
-from gpu_util import dev
+from gen import custom_attn_inputs, make_layer_inputs
+from gpu_util import attn_tensors, dev
 from serving_util import make_step
 
 pytestmark = pytest.mark.gpu
@@ -73,12 +73,74 @@ def layer_call(seed):
             [20 * D * 2, hstu.hstu_layer_step_workspace_bytes(20, D, li.H, li.d, 20)])
 
 
+def dense_call(which):
+    """The calls on whole batches: their inputs for a seed, the call, what it allocates."""
+    def make(seed):
+        inp = custom_attn_inputs([300, 17, 90], H=4, d=64, num_pos=64, num_buckets=64,
+                                 dtype="f32" if which.endswith("f32") else "bf16", seed=seed)
+        t = attn_tensors(inp)
+        T, F = t["q"].shape[0], 256
+        args = [t[n] for n in ("seq_offsets", "timestamps", "pos_bias", "time_bias", "max_seqlen")]
+        qkv = [t[n] for n in "qkv"]
+        g = torch.Generator().manual_seed(seed)
+        x, u = (torch.randn(T, F, generator=g).to(BF).cuda() for _ in range(2))
+        W, W2 = torch.randn(4 * F, F, generator=g).to(BF).cuda() / 16, torch.eye(F, dtype=BF).cuda()
+        if which.startswith("attn_fwd"):
+            bf = which == "attn_fwd"
+            ws = hstu.hstu_attn_workspace_bytes(3, T, inp.max_seqlen, 4, 64) if bf else 16
+            return lambda **kw: hstu.hstu_attn_fwd(*qkv, *args, **kw), [T * F * (2 if bf else 4), ws]
+        if which == "attn_bwd":
+            ws = hstu.hstu_attn_bwd_workspace_bytes(3, T, inp.max_seqlen)
+            return lambda **kw: hstu.hstu_attn_bwd(*qkv, u.view(T, 4, 64), *args, **kw), [T * F * 4] * 3 + [ws]
+        if which == "attn_bwd_f32":
+            dout = u.float().view(T, 4, 64)
+            return (lambda **kw: hstu.hstu_attn_bwd_f32(*qkv, dout, *args, **kw),
+                    [T * F * 4] * 3)
+        if which == "bias_indices":
+            return (lambda **kw: hstu.hstu_debug_bias_indices(args[0], args[1], 64, 64, **kw),
+                    [T * T * 2] * 2)
+        if which == "linear":
+            return lambda **kw: hstu.hstu_linear_fwd(x, W, **kw), [T * 4 * F * 2]
+        if which == "layernorm":
+            return lambda **kw: hstu.hstu_layernorm_fwd(x, **kw), [T * F * 2]
+        if which == "layernorm_gate":
+            return lambda **kw: hstu.hstu_layernorm_gate_fwd(x, u, **kw), [T * F * 2]
+        if which == "layernorm_fp8":
+            return lambda **kw: hstu.hstu_layernorm_fp8_fwd(x, **kw), [T * F, T * 4]
+        if which == "layernorm_gate_fp8":
+            return lambda **kw: hstu.hstu_layernorm_gate_fp8_fwd(x, u, **kw), [T * F, T * 4]
+        if which == "quant_rows":
+            return lambda **kw: hstu.hstu_quant_rows_e4m3(x, **kw), [T * F, T * 4]
+        if which == "layer":
+            ws = hstu.hstu_layer_workspace_bytes(T, 3, F, 4, 64, inp.max_seqlen)
+            return lambda **kw: hstu.hstu_layer_fwd(x, W, W2, *args[:4], 4, 64, args[4], **kw), [T * F * 2, ws]
+        q1, q2 = hstu.hstu_quant_rows_e4m3(W), hstu.hstu_quant_rows_e4m3(W2)
+        if which == "linear_fp8":
+            xq = hstu.hstu_quant_rows_e4m3(x)
+            return lambda **kw: hstu.hstu_linear_fp8_fwd(*xq, *q1, **kw), [T * 4 * F * 2]
+        ws = hstu.hstu_layer_fp8_workspace_bytes(T, 3, F, 4, 64, inp.max_seqlen)
+        return lambda **kw: hstu.hstu_layer_fp8_fwd(x, *q1, *q2, *args[:4], 4, 64, args[4], **kw), [T * F * 2, ws]
+    return make
+
+
 CALLS = {"plan": plan_call, "quant": quant_call, "linear_w4": linear_call, "attn": attn_call,
          "layer_step": layer_call}
+CALLS.update((name, dense_call(name)) for name in (
+    "attn_fwd", "attn_fwd_f32", "attn_bwd", "attn_bwd_f32", "bias_indices", "linear", "layernorm",
+    "layernorm_gate", "layernorm_fp8", "layernorm_gate_fp8", "quant_rows", "layer", "linear_fp8",
+    "layer_fp8"))
 
 
 def tensors(r):
     return [t.clone() for t in (r if isinstance(r, tuple) else (r,))]
+
+
+def assert_same(name, got, want):
+    for g, w in zip(got, want):
+        if name.startswith("attn_bwd"):         # (sums by atomics, in any order)
+            assert float((g - w).norm()) <= 1e-4 * float(w.norm())
+        else:
+            assert torch.equal(g, w)
 
 
 @pytest.mark.parametrize("name", CALLS)
@@ -91,8 +153,7 @@ def test_outputs_are_not_memory_that_queued_work_writes(name):
     queued(sizes)
     got = call(stream=side)
     torch.cuda.synchronize()
-    for g, w in zip(tensors(got), want):
-        assert torch.equal(g, w)
+    assert_same(name, tensors(got), want)
     assert hstu.hstu_device_status() == 0
 
 
@@ -112,8 +173,7 @@ def test_results_outlive_their_readers_on_the_current_stream(name):
     for _ in range(3):
         other(stream=side)
     torch.cuda.synchronize()
-    for g, w in zip(copies, want):
-        assert torch.equal(g, w)
+    assert_same(name, copies, want)
     assert hstu.hstu_device_status() == 0
 
 
@@ -130,6 +190,5 @@ def test_the_default_stream_given_while_another_is_current(name, handle):
         same = call(stream=torch.cuda.current_stream())
         torch.cuda.synchronize()
         for r in (got, same):
-            for g, w in zip(tensors(r), want):
-                assert torch.equal(g, w)
+            assert_same(name, tensors(r), want)
     assert hstu.hstu_device_status() == 0
