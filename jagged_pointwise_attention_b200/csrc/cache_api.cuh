@@ -347,8 +347,12 @@ hstu_status_t make_cached(hstu_dtype_t dtype, const void* q, int64_t q_tok_strid
     a.heads = static_cast<PartHead*>(workspace);
     a.parts = reinterpret_cast<float*>(a.heads + (dtype == HSTU_DTYPE_F32 ? kSimtBlocks : kMmaBlocks));
     a.part_rows = cached_part_rows(dtype, max_new, d_v);
-    return validate_cached(dtype, a, page_size, workspace, workspace_bytes,
-                           hstu_attn_cached_workspace_bytes(dtype, max_new, d_v));
+    const hstu_status_t st = validate_cached(dtype, a, page_size, workspace, workspace_bytes,
+                                             hstu_attn_cached_workspace_bytes(dtype, max_new, d_v));
+    // No sequence brings more: a generous bound picks no other kernel, adds no
+    // blocks and overflows no count of tiles.
+    if (a.max_new > max_seqlen) a.max_new = max_seqlen;
+    return st;
 }
 
 hstu_status_t launch_cached(hstu_dtype_t dtype, const CachedArgs& a, cudaStream_t s) {
@@ -431,9 +435,10 @@ hstu_status_t hstu_cache_plan(const int32_t* ctx_lens, const int64_t* new_offset
     CachePlanArgs a{ctx_lens, new_offsets, B, total_new, shift, free_pages, num_free, free_start,
                     block_table, table_stride, max_pages, slots, free_end, 1};
     // up to two blocks an SM over the sequences, then over each block's tokens
-    int s = (B + 295) / 296;
-    a.seqs_per_block = s > kPlanSeqs ? kPlanSeqs : s;
-    const unsigned gx = static_cast<unsigned>((B + a.seqs_per_block - 1) / a.seqs_per_block);
+    const int64_t s = (static_cast<int64_t>(B) + 295) / 296;
+    a.seqs_per_block = static_cast<int>(s > kPlanSeqs ? kPlanSeqs : s);
+    const unsigned gx = static_cast<unsigned>((static_cast<int64_t>(B) + a.seqs_per_block - 1) /
+                                              a.seqs_per_block);
     const int64_t per = (total_new / gx + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
     const int64_t most = gx >= 296 ? 1 : 296 / gx;
     const unsigned gy = static_cast<unsigned>(per < 1 ? 1 : per < most ? per : most);

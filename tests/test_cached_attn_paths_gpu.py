@@ -190,3 +190,17 @@ def test_padded_batches_and_shared_pages(d, most, dtype):
     hstu.hstu_cache_append(ones, ones, None, slots, kc, vc, None)
     ok()
     assert kc.float().sum().item() == T * 2 * d == vc.float().sum().item()
+
+
+@pytest.mark.parametrize("dtype,d,kind", [(BF, 32, "chain"), (BF, 64, "chain"), (BF, 128, "chain"),
+                                          (torch.float32, 32, "chain"), (BF, 64, "tree")])
+@pytest.mark.parametrize("ctx,new", [([100, 3], [5, 20]), ([900, 40], [6, 9])], ids=["short", "long"])
+def test_max_new_above_what_a_sequence_can_bring(dtype, d, kind, ctx, new):
+    """max_new is a bound: one above max_seqlen gives the bits that max_seqlen gives."""
+    s = make_step(ctx, new, kind, 2, d, d, 16, dtype, seed=d, max_seqlen=max(ctx) + 30)
+    N = s.max_seqlen
+    for most in ((2 ** 31 - 1, 2 ** 31 - 9, N + 1) if kind == "chain" else (256,)):
+        got = call_attn(hstu, s, max_new=most)
+        ok()
+        assert torch.equal(got, call_attn(hstu, s, max_new=min(most, N)))
+        check_attn(s, got)
