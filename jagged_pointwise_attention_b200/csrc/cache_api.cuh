@@ -20,6 +20,12 @@ int page_shift(int32_t page_size) {
     return s;
 }
 
+// Addresses of arrays of `bytes`-byte elements (null counts as aligned).
+template <typename... P>
+bool aligned_to(uintptr_t bytes, const P*... p) {
+    return ((reinterpret_cast<uintptr_t>(p) | ... | uintptr_t{0}) & (bytes - 1)) == 0;
+}
+
 bool cache_size_ok(int32_t num_pages, int32_t page_size) {
     return num_pages >= 1 && page_size >= 1 &&
            static_cast<int64_t>(num_pages) * page_size <= 0x7fffffff;
@@ -52,6 +58,9 @@ hstu_status_t validate_cached(hstu_dtype_t dtype, const CachedArgs& c, int32_t p
     if (c.k_page < (page_size - 1) * c.k_tok + rq || c.v_page < (page_size - 1) * c.v_tok + rv)
         return HSTU_ERR_INVALID_ARG;
     if (c.tsc && (c.tsc_page < page_size || reinterpret_cast<uintptr_t>(c.tsc) % 8))
+        return HSTU_ERR_INVALID_ARG;
+    if (!aligned_to(8, c.off, c.ts) || !aligned_to(4, c.table, c.ctx, c.parents, c.pos, c.tb) ||
+        (dtype == HSTU_DTYPE_F32 && !aligned_to(4, c.q, c.k, c.v, c.out)))
         return HSTU_ERR_INVALID_ARG;
     if (dtype == HSTU_DTYPE_BF16) {
         if (!aligned16(c.q) || !aligned16(c.k) || !aligned16(c.v) || !aligned16(c.out))
@@ -284,7 +293,7 @@ hstu_status_t make_append(hstu_dtype_t dtype, const void* k, int64_t k_stride, c
     mix = reinterpret_cast<uint64_t>(k) | reinterpret_cast<uint64_t>(v) |
           reinterpret_cast<uint64_t>(k_cache) | reinterpret_cast<uint64_t>(v_cache) | a.k_stride |
           a.v_stride | a.kc_page | a.kc_tok | a.vc_page | a.vc_tok | a.k_bytes | a.v_bytes;
-    return mix % e ? HSTU_ERR_INVALID_ARG : HSTU_OK;
+    return mix % e || !aligned_to(8, timestamps, slots) ? HSTU_ERR_INVALID_ARG : HSTU_OK;
 }
 
 hstu_status_t launch_append(const CacheAppendArgs& a, uint64_t mix, cudaStream_t s) {
@@ -431,6 +440,9 @@ hstu_status_t hstu_cache_plan(const int32_t* ctx_lens, const int64_t* new_offset
     if (!cache_size_ok(max_pages, page_size)) return HSTU_ERR_UNSUPPORTED;
     if (!ctx_lens || !new_offsets || !free_start || !block_table || !free_end || free_end == free_start ||
         (num_free > 0 && !free_pages) || (total_new > 0 && !slots))
+        return HSTU_ERR_INVALID_ARG;
+    if (!aligned_to(8, new_offsets, slots) ||
+        !aligned_to(4, ctx_lens, free_pages, free_start, block_table, free_end))
         return HSTU_ERR_INVALID_ARG;
     CachePlanArgs a{ctx_lens, new_offsets, B, total_new, shift, free_pages, num_free, free_start,
                     block_table, table_stride, max_pages, slots, free_end, 1};

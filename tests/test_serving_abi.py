@@ -112,3 +112,21 @@ def test_binding_refuses(lib):
     with pytest.raises((ValueError, RuntimeError, AssertionError)):
         hstu.hstu_cache_plan(z(1, dtype=torch.int32), off, z(1, dtype=torch.int32),
                              z(1, dtype=torch.int32), z(1, 4, dtype=torch.int32), 16, 2)
+
+
+def test_arrays_off_their_elements_alignment(lib):
+    """An address between two elements would fault on the device."""
+    def plan(ctx=16, off=16, free=16, start=16, table=16, slots=16, end=32):
+        return lib.hstu_cache_plan(ctx, off, 2, 4, 16, free, 4, start, table, 8, 8, slots, end, None)
+    for kw in (dict(ctx=18), dict(off=20), dict(free=17), dict(start=18), dict(table=18), dict(slots=20),
+               dict(end=34)):
+        assert plan(**kw) == INV, kw
+
+    def append(ts=16, slots=16):
+        return lib.hstu_cache_append(1, 16, 128, 16, 128, ts, slots, 4, 2, 64, 64, 16, 2048, 128, 16, 2048,
+                                     128, 16, 16, 4, 16, None)
+    for kw in (dict(ts=20), dict(slots=20)):
+        assert append(**kw) == INV, kw
+    for kw in (dict(off=20), dict(ts=20), dict(table=18), dict(ctx=17), dict(par=18), dict(pos=18),
+               dict(tb=18), dict(dt=0, q=18), dict(dt=0, kc=18), dict(dt=0, vc=17), dict(dt=0, out=18)):
+        assert cached(lib, **kw) == INV, kw
