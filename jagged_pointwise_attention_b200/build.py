@@ -45,10 +45,27 @@ def needs_build(out: str = LIB) -> bool:
     return any(os.path.getmtime(s) > t for s in _sources())
 
 
+def binding_tag() -> str:
+    """What _serving.so fits, written into it: torch and its C++ ABI, CPython."""
+    import torch
+
+    return "built for torch %s, C++11 ABI %d, CPython %d.%d" % (
+        torch.__version__, int(torch._C._GLIBCXX_USE_CXX11_ABI), *sys.version_info[:2])
+
+
+def binding_needs_build(out: str = BINDING) -> bool:
+    if not os.path.exists(out):
+        return True
+    newest = max(os.path.getmtime(BINDING_SRC), os.path.getmtime(os.path.join(INCLUDE, "hstu.h")))
+    if os.path.getmtime(out) < newest:
+        return True
+    with open(out, "rb") as f:
+        return binding_tag().encode() + b"\0" not in f.read()
+
+
 def build_binding(force: bool = False) -> str:
     """_serving.so against the installed torch (its headers, its C++ ABI)."""
-    newest = max(os.path.getmtime(BINDING_SRC), os.path.getmtime(os.path.join(INCLUDE, "hstu.h")))
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+    if not force and not binding_needs_build(BINDING):
         return BINDING
     import torch
 
@@ -58,6 +75,7 @@ def build_binding(force: bool = False) -> str:
     subprocess.check_call([
         os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
         "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+        '-DHSTU_BINDING_TAG="%s"' % binding_tag(),
         "-I", INCLUDE, "-isystem", os.path.join(tdir, "include"),
         "-isystem", os.path.join(tdir, "include", "torch", "csrc", "api", "include"),
         "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"),
@@ -67,9 +85,7 @@ def build_binding(force: bool = False) -> str:
     return BINDING
 
 
-def build(force: bool = False, verbose: bool = False, out: str = LIB, extra=()) -> str:
-    if out == LIB:
-        build_binding(force)
+def build_library(force: bool, verbose: bool, out: str, extra) -> str:
     if not force and not needs_build(out):
         return out
     nvcc = os.environ.get("NVCC", "nvcc")
@@ -78,6 +94,14 @@ def build(force: bool = False, verbose: bool = False, out: str = LIB, extra=()) 
         "-I", INCLUDE, "-I", CSRC, "-o", tmp, os.path.join(CSRC, "hstu_api.cu")]
     subprocess.check_call(cmd)
     os.replace(tmp, out)
+    return out
+
+
+def build(force: bool = False, verbose: bool = False, out: str = LIB, extra=()) -> str:
+    """The library, which needs no torch, then the binding."""
+    build_library(force, verbose, out, extra)
+    if out == LIB:
+        build_binding(force)
     return out
 
 

@@ -441,7 +441,8 @@ PyObject* bind(PyObject*, PyObject* args) {
 PyMethodDef methods[] = {FAST(cache_plan), FAST(cache_append), FAST(attn_cached), FAST(quant_w4),
                          FAST(linear_w4), {"bind", bind, METH_VARARGS, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serving", nullptr, -1, methods};
+// The build reads the tag back from the file, to see whether it still fits.
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serving", HSTU_BINDING_TAG, -1, methods};
 
 }  // namespace
 
