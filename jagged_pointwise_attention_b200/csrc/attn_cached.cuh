@@ -390,14 +390,12 @@ __global__ void __launch_bounds__(kJoinThreads) attn_cached_join_kernel(const Ca
 
 // ------------------------------------------------------------------ the tree
 
-// Who sees whom among a sequence's new tokens, for one tile of NQ queries
-// (64-bit word w of key m: queries 64w .. 64w + 63 of the tile that see m) and
-// the depth of every new token.
+// Who sees whom among a sequence's new tokens (word w of key m: which of the
+// queries 32w .. 32w + 31 see m) and the depth of every new token.
 struct alignas(16) TreeSmem {
     uint32_t seen[kMaxTree / 32][kMaxTree];     // [query / 32][key]: bit of the query
     int16_t depth[kMaxTree];
     int16_t parent[kMaxTree];
-    int deepest;                                // greatest depth
 };
 
 // Built by `nt` threads (index t), which `sync` holds together; a parent that
@@ -406,7 +404,6 @@ template <typename Sync>
 __device__ __forceinline__ void build_tree(const CachedArgs& a, const CachedSeq& s, TreeSmem& tree,
                                            int t, int nt, Sync sync) {
     sync();                                     // the previous tree is no longer read
-    if (t == 0) tree.deepest = 0;
     const int words = (s.n + 31) / 32;
     for (int m = t; m < s.n; m += nt) {
         const int p = a.parents[s.off + m];
@@ -423,7 +420,6 @@ __device__ __forceinline__ void build_tree(const CachedArgs& a, const CachedSeq&
             ++d;
         }
         tree.depth[m] = static_cast<int16_t>(d);
-        atomicMax(&tree.deepest, d);
     }
     sync();
 }

@@ -4,14 +4,15 @@
 //
 // Bound by latencies and the cache's bytes, so the layout serves the loads.
 // Keys come in groups of 16, which never cross a page. Each warp of a block
-// (four for whole sequences, so that three blocks share an SM, twelve along the
-// line) takes every n-th group of the block's part and feeds itself: its lane
+// (four for whole sequences, so that blocks share an SM, twelve along the line)
+// takes every n-th group of the block's part and feeds itself: its lane
 // 0 issues the TMA loads of a group's K and V rows into the warp's own ring,
 // groups ahead and across item borders, so no barrier of the block stands
 // between two loads. The tokens' timestamps ride on the same barrier as 8-byte
 // copies. 128 sequences of 20 to 200 tokens, 2 heads of 64, one new token: 9.6
-// us with its launch, of which about 7 are one chain of dependent loads
-// (lengths, page numbers, keys and values).
+// us with its launch, of which about 7 are dependent loads: lengths, page
+// numbers, keys and values, and above 128 tokens keys and values once more (a
+// warp has two groups in flight and up to four to read).
 //
 // Products run as 16 keys x 8 queries (m16n8k16), transposed against the usual
 // order: S^T = K Q^T and O^T = V^T P^T. So the long axis fills the 16 rows, a
@@ -29,9 +30,12 @@ constexpr int kMmaKeys = 16;            // keys of a group
 
 template <int D, int NT, bool WHOLE>
 struct CachedMmaSmem {
-    // Whole items: four warps, so that three blocks share an SM.
+    // Whole items: four warps, so that blocks share an SM. 92 KB a block at heads
+    // of 128 (rings 64, sums 17, tree 9), 52 at 64 and 32 at 32: two blocks an SM,
+    // four and six; launched for two, and for three at 64 and 32.
     static constexpr int kWarps = WHOLE ? 4 : 12;
     static constexpr int kThreads = kWarps * 32;
+    static constexpr int kBlocksPerSm = !WHOLE ? 1 : D == 128 ? 2 : 3;
     static constexpr int kNQ = 8 * NT;
     static constexpr int kRowBytes = D >= 64 ? 128 : 64;    // bytes of a box row
     static constexpr int kBoxes = D / 64 > 0 ? D / 64 : 1;
@@ -86,7 +90,8 @@ __device__ __noinline__ float2 odd_sum(const CachedArgs& a, const uint32_t* odd,
 // WHOLE: block i takes item i whole (short sequences: no part, no join, no
 // search); otherwise an equal part of the line.
 template <int D, int NT, bool WHOLE>
-__global__ void __launch_bounds__(CachedMmaSmem<D, NT, WHOLE>::kThreads, WHOLE ? 3 : 1)
+__global__ void __launch_bounds__(CachedMmaSmem<D, NT, WHOLE>::kThreads,
+                                  CachedMmaSmem<D, NT, WHOLE>::kBlocksPerSm)
 attn_cached_mma_kernel(const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV,
                        const __grid_constant__ CachedArgs a, int qtiles) {

@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_cached_simt_kernel(const Ca
             ahead = look(k0 + kSimtKeys + tid);
             cp_async_wait_all();
             __syncthreads();
-            // scores of key tid % 64, queries 4 (tid / 64) ..
+            // scores of key tid % 64 and half of the queries
             {
                 constexpr int HALF = R / 2;
                 const int r = tid % kSimtKeys, half = tid / kSimtKeys, i0 = half * HALF;
