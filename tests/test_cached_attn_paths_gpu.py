@@ -7,7 +7,7 @@ import torch
 
 import jagged_pointwise_attention_b200 as hstu
 from jagged_pointwise_attention_b200 import _native
-from serving_util import call_attn, check_attn, make_step, oracle
+from serving_util import attn_tolerance, call_attn, check_attn, make_step, oracle
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -204,3 +204,57 @@ def test_max_new_above_what_a_sequence_can_bring(dtype, d, kind, ctx, new):
         ok()
         assert torch.equal(got, call_attn(hstu, s, max_new=min(most, N)))
         check_attn(s, got)
+
+
+@pytest.mark.parametrize("dtype,d,kind", [(BF, 64, "tree"), (BF, 128, "chain"), (BF, 32, "tree"),
+                                          (F32, 32, "chain")])
+def test_thousands_of_sequences_along_the_line(dtype, d, kind):
+    """Several sequences a thread in the search of the line; many without new
+    tokens or without a context; a long one among them keeps all on the line."""
+    rng = np.random.default_rng(d)
+    ctx = [int(x) for x in rng.integers(0, 40, 5000)]
+    new = [int(x) for x in rng.integers(0, 3, 5000)]
+    ctx[3333], new[3333] = 1500, 5
+    s = make_step(ctx, new, kind, 1, d, d, 16, dtype, seed=d)
+    got = call_attn(hstu, s)
+    ok()
+    check_attn(s, got)
+
+
+def chain_oracle(s):
+    """`oracle` for one sequence whose new tokens are a chain, all pairs at once."""
+    c, n, H, N = s.ctx[0], s.new[0], s.q.shape[1], s.max_seqlen
+    g = [int(s.table[0, j // s.page]) for j in range(c + n)]
+    r = [j % s.page for j in range(c + n)]
+    K, V = s.kc[g, r].double().numpy(), s.vc[g, r].double().numpy()
+    Q, tk = s.q.double().numpy(), s.tsc[g, r].numpy()
+    i, j = np.arange(c, c + n)[:, None], np.arange(c + n)[None, :]
+    rel = np.clip(i - j, 0, s.pos.shape[1] - 1)
+    dt = np.maximum(s.ts[:, None] - tk[None, :], 1)
+    bucket = np.minimum(np.frexp(dt.astype(np.float64))[1] - 1, s.tb.shape[1] - 1)
+    out, A, E = (np.zeros((n, H, V.shape[2])) for _ in range(3))
+    for h in range(H):
+        x, e = Q[:, h] @ K[:, h].T, np.abs(Q[:, h]) @ np.abs(K[:, h]).T
+        for add in (s.pos.double().numpy()[h][rel], s.tb.double().numpy()[h][bucket]):
+            x, e = x + add, e + np.abs(add)
+        p = np.where(j <= i, x / (1 + np.exp(-x)), 0.0)
+        e = np.where(j <= i, 1.1 * (Q.shape[2] + 4) * 2 * 2.0 ** -24 * e, 0.0)
+        a = np.abs(V[:, h])
+        out[:, h], A[:, h], E[:, h] = p @ V[:, h] / N, np.abs(p) @ a / N, e @ a / N
+    return out, A, E
+
+
+@pytest.mark.parametrize("dtype,d,H", [(BF, 64, 2), (BF, 128, 1), (BF, 32, 1), (F32, 64, 1)])
+@pytest.mark.parametrize("ctx,new", [(700, 2311), (0, 3001)])
+def test_thousands_of_new_tokens_in_a_row(dtype, d, H, ctx, new):
+    """A piece of a prompt, and a whole one. (Time differences below 2^53, so frexp
+    is exact.)"""
+    s = make_step([ctx], [new], "chain", H, d, d, 64, dtype, seed=d + new)
+    got = call_attn(hstu, s).double().cpu().numpy()
+    ok()
+    want, A, E = chain_oracle(s)
+    few = make_step([50], [9], "chain", H, d, d, 16, dtype, seed=1)
+    assert all(np.allclose(x, y, rtol=1e-12, atol=1e-15) for x, y in zip(chain_oracle(few), oracle(few)))
+    tol = attn_tolerance(s, want, A, E)
+    assert np.all(np.isfinite(got)) and np.all(np.abs(got - want) <= tol), \
+        "off by up to %.3g times the bound" % np.max(np.abs(got - want) / tol)

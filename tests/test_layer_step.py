@@ -275,3 +275,32 @@ def test_a_refused_call_leaves_the_cache_and_the_output(group):
     call()
     torch.cuda.synchronize()
     assert hstu.hstu_device_status() == 0 and not torch.equal(srv.tsc, before[2])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("group", [0, 64])
+@pytest.mark.parametrize("D,H", [(512, 8), (256, 4), (1024, 32)])
+def test_heads_of_64(group, D, H):
+    """Other widths of the layer and its heads: prompts, then a token or a few."""
+    lens, d = [170, 33], 64
+    li = make_layer_inputs(5, lengths_override=lens)
+    rng = np.random.default_rng(D)
+    F = H * d
+    li.H, li.d = H, d
+
+    def matrix(rows, cols):
+        return round_to_bf16((rng.standard_normal((rows, cols)) / np.sqrt(cols)).astype(np.float32))
+    li.x, li.W1, li.W2 = round_to_bf16(rng.standard_normal((sum(lens), D)).astype(np.float32)), \
+        matrix(4 * F, D), matrix(D, F)
+    li.pos_bias, li.time_bias = ((0.1 * rng.standard_normal((H, n))).astype(np.float32) for n in (64, 128))
+    W1, W2, o1, o2 = weights(li, group)
+    want = oracle.layer(li.seq_offsets, li.x, o1, o2, H, d, li.timestamps, li.pos_bias, li.time_bias,
+                        li.max_seqlen, ln_eps=li.ln_eps)
+    srv = Server(li, 16, 32, W1, W2)
+    off = li.seq_offsets
+    for new in ([140, 20], [1, 1], [20, 12], [9, 0]):
+        rows = np.concatenate([np.arange(off[b] + srv.ctx[b], off[b] + srv.ctx[b] + n)
+                               for b, n in enumerate(new)]).astype(np.int64)
+        got = srv.step(li.x[rows], li.timestamps[rows], new)
+        assert_bf16_close(got, want[rows], "step %s" % (new,))
+    assert srv.ctx == lens
