@@ -471,8 +471,11 @@ hstu_status_t hstu_cache_append(hstu_dtype_t dtype, const void* k, int64_t k_str
  *          + time_bias[h][clamp(floor(log2(max(1, ts_i - ts_j))), 0, NB - 1)]
  *   out_i = (1 / max_seqlen) * sum_{j seen by i} silu(s_ij) v_j
  * so a chain gives the rows that hstu_attn_fwd gives for these tokens of the
- * whole sequence. What lies in the cache outside a sequence's tokens, and the
- * values of tokens that a query does not see, do not matter (they may be NaN).
+ * whole sequence. With bf16, scores, silu and sums are held in 32 bits, each
+ * silu(s_ij) is rounded to bf16 for its product with v_j (as in hstu_attn_fwd) and
+ * the result once more; fp32 rounds to nothing less. What lies in the cache
+ * outside a sequence's tokens, and the values of tokens that a query does not see,
+ * do not matter (they may be NaN).
  *   q : device [total_new, H, d_qk] of `dtype`, out : [total_new, H, d_v]; the
  *       rows of every sequence's new tokens are written, nothing else is
  *   max_new : the most new tokens a sequence has (>= 1; at most 256 with
@@ -485,11 +488,11 @@ hstu_status_t hstu_cache_append(hstu_dtype_t dtype, const void* k, int64_t k_str
  * Supported: bf16 with d_qk == d_v in {32, 64, 128} (bases 16-byte aligned,
  * strides multiples of 8); fp32 with d_qk, d_v <= 128. A sequence with
  * impossible numbers (longer than max_seqlen or its table row, more new tokens
- * than max_new) is left out, a page outside the cache counts as no tokens, a
- * parent that is not before its token counts as -1; all report
- * HSTU_ERR_BAD_INPUT. Pages may be shared by sequences (a common prefix).
- * Results are the same bits on every run. One launch, or two where sequences
- * may be split over blocks. */
+ * than max_new) is left out (where offsets decrease, rows that two sequences
+ * name are not specified), a page outside the cache counts as no tokens, a parent
+ * that is not before its token counts as -1; all report HSTU_ERR_BAD_INPUT.
+ * Pages may be shared by sequences (a common prefix). Results are the same bits on
+ * every run. One launch, or two where sequences may be split over blocks. */
 size_t hstu_attn_cached_workspace_bytes(hstu_dtype_t dtype, int32_t max_new, int32_t d_v);
 hstu_status_t hstu_attn_cached_fwd(hstu_dtype_t dtype, const void* q, int64_t q_tok_stride,
                                    const void* k_cache, int64_t k_page_stride,
@@ -524,9 +527,10 @@ hstu_status_t hstu_quant_groups_w4(const void* W, int64_t ldw, int64_t N, int32_
  * weights' bytes. Codes and scales as hstu_quant_groups_w4 writes them; x, y,
  * residual bf16, bias fp32 [N] or NULL, epilogues as hstu_linear_fwd. Products
  * are exact in fp32 before the scale, sums are fp32, and the result is rounded
- * once. K % 128 == 0, 1 <= N <= 2^31 - 65; x and codes 16-byte aligned, ldx % 8
- * == 0, ldc % 16 == 0. For many rows hstu_linear_fwd and hstu_linear_fp8_fwd are the
- * faster calls: the weights are read once for every 64 rows. */
+ * once. K % 128 == 0, 1 <= N <= 2^31 - 65, M <= 524280; x and codes 16-byte
+ * aligned, ldx % 8 == 0, ldc % 16 == 0. For many rows hstu_linear_fwd and
+ * hstu_linear_fp8_fwd are the faster calls (8192 to 16384: 32 rows 59 us here and 66
+ * in bf16, 64 rows 92 and 66). */
 hstu_status_t hstu_linear_w4_fwd(const void* x, int64_t ldx, int64_t M, int32_t K, const void* codes,
                                  int64_t ldc, const void* scales, int64_t lds, int32_t group,
                                  int32_t N, const float* bias, hstu_epilogue_t epilogue,
@@ -544,9 +548,10 @@ size_t hstu_layer_step_workspace_bytes(int64_t total_new, int32_t D, int32_t H, 
  * possible. w4_group 0: W1 and W2 are bf16 as in hstu_layer_fwd, s1 and s2 are
  * not read. w4_group 32, 64 or 128: W1 and W2 are codes [4 H d, D/2] and
  * [D, H d/2] with scales s1 [4 H d, D/group] and s2 [D, H d/group] as
- * hstu_quant_groups_w4 writes them, rows without gaps. Sizes as hstu_layer_fwd;
- * cache, batch and the rest as hstu_cache_append and hstu_attn_cached_fwd; rows
- * of out behind the last sequence are not specified. */
+ * hstu_quant_groups_w4 writes them, rows without gaps, and total_new <= 524280.
+ * Sizes as hstu_layer_fwd; cache, batch and the rest as hstu_cache_append and
+ * hstu_attn_cached_fwd; rows of out behind the last sequence are not specified. A
+ * refused call has changed nothing. */
 hstu_status_t hstu_layer_step_fwd(const void* x, int64_t total_new, int32_t D, const void* W1,
                                   const void* s1, const float* b1, const void* W2, const void* s2,
                                   const float* b2, int32_t w4_group, const float* ln_gamma,

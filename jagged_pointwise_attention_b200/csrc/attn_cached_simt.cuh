@@ -5,10 +5,14 @@
 // or 16 where there are more new tokens (each tile reads its keys again).
 // A tile's keys, values and timestamps are copied to shared memory at once
 // (cp.async; rows padded by four floats, so the 16-byte reads of eight lanes
-// fall into different banks), its pages looked up a tile ahead: bound by the
-// latency of these copies, with about two tiles a block. Scores: thread t has
-// key t % 64 and half of the queries. Values: thread t has column t %
-// DMAX of the output and every (128 / DMAX)-th key.
+// fall into different banks), its pages looked up a tile ahead. There is one
+// buffer, so a tile's copies are waited for before its arithmetic and overlap only
+// with other blocks' (64 sequences of 200 to 1100 tokens, five in a row, 2 heads
+// of 32: 29 us, the bytes alone 3.4). With many queries the arithmetic on CUDA
+// cores and the keys read again for every 16 of them count (32 sequences of 256 to
+// 2048, 64 drafted tokens: 211 to 262 us, the bytes alone 12.7). Scores: thread t
+// has key t % 64 and half of the queries. Values: thread t has column t % DMAX of
+// the output and every (128 / DMAX)-th key.
 #pragma once
 
 #include "attn_cached.cuh"

@@ -28,19 +28,31 @@
 //   17    an item's Q and its tables (positions, times, who sees whom)
 //   18    each step's window of position biases
 // A load takes 2.5 to 3 us while HBM is busy, so nothing asks for its data when
-// it needs it. All roles run at once, so their code together has to stay in the
+// it needs it. All roles run at once, so what they run together has to stay in the
 // instruction cache: loops are short, waits are out of line, and only one role
-// knows how to walk the line. (At 120 KB of code instead of about a third of
-// that, instruction fetches were the bound and a step took twice as long.)
+// knows how to walk the line. (82 KB of code, of which about a third runs in the
+// steady state; at 122 KB instruction fetches were the bound, and the 64-token
+// trees took 86 us when this brought them to 62.)
 //
-// Bound by the cache's bytes for few queries, from about 64 on by the pointwise
-// stage (two SFU operations and about fourteen others a pair). 32 sequences of
-// 256 to 4096 tokens, 4 heads of 128, with the join: 8 new tokens 42 us, 32 44,
-// 64 53, 128 89, against 23 us for the bytes (150 MB) alone. One token over 16
-// sequences of up to 8192: 43 us (180 MB, 4.2 TB/s). Start-up to the first
-// product takes about 7 us, the join 3 to 5. Sixteen pointwise warps gained a
-// tenth at 128 queries and lost as much at one; the approximate tanh would save
-// one of the two SFU operations and miss silu's bf16 step.
+// Bound by the cache's bytes and a launch's start for few queries. From about 64
+// on by latency in the pointwise stage: no unit is full (64-token trees, heads of
+// 128: SFU 21%, issue slots 40%, tensor pipe 10%; 128 tokens, heads of 64: 32, 47
+// and 11%), but the TMEM load, table reads, exp2, reciprocal, pack and store of
+// eight queries follow one another, in two warps a scheduler. 32 sequences of 256
+// to 4096 tokens with the join, 4 heads of 128 (8 of 64): 8 new tokens 42 us (47),
+// 32 44 (53), 64 53 (78), 128 89 (136), against 23 us for the bytes (150 MB)
+// alone. One token over 16 sequences of up to 8192: 43 us (180 MB, 4.2 TB/s). A
+// launch has found its line after 3 us and issues the first product at 7 to 8; a
+// tree's first weights come at 12, since one warp builds an item's tree for its
+// tables (ready at 11). The join takes 3 to 5. Sixteen pointwise warps gained a
+// tenth at 128 queries and lost 2% at one; the approximate tanh would save one of
+// the two SFU operations and miss silu's bf16 step.
+//
+// P is rounded to bf16, the type that a product with a bf16 V takes: at most 2^-8
+// of a weight, like the dense forward. Outputs are then 0.0023 to 0.0024 (relative,
+// root mean square) from the 64-bit ones, of which their own rounding is 0.0017.
+// Two bf16 terms a weight would keep it, for twice the second product and twice
+// P's stores in the stage that is the bound.
 #pragma once
 
 #include "attn_cached.cuh"

@@ -188,7 +188,7 @@ int64_t cached_whole_items(const CachedArgs& a, int rows) {
 
 // Heads of 64 and 128: the tcgen05 kernel, but for up to eight new tokens over
 // sequences that are taken whole, and up to sixteen over those of up to 256
-// tokens. (300 sequences of 200, 12 new tokens, 2 heads of 128: 36 us against
+// tokens. (300 sequences of 200, 12 new tokens, 2 heads of 128: 34 us against
 // 43, 4 of 64: 36 and 61; of 900, 16 new tokens, heads of 128: 61 and 46.)
 template <int D>
 hstu_status_t run_cached_bf16(const CachedArgs& a, cudaStream_t stream) {

@@ -43,20 +43,23 @@ __device__ __forceinline__ void w4_store(const LinearW4Args& a, int64_t m, int n
 // fragment row hold 32 consecutive ones, so every m16n8k16 product stays inside
 // one scale group whatever its size.
 //
-// Codes become bf16 without a conversion: 0x4300 | c is 128 + c, and minus 136
-// is exact. c - 8 and x are exact bf16, so a group's products and their sum are
-// plain fp32; the scale multiplies the group's sum. The order of k inside a
-// fragment is free as long as W and x share it: nibbles i and i + 4 of a word
-// are one register, and x is paired to match.
+// Codes become bf16 without a conversion, a published way to unpack 4-bit weights
+// whose constants follow from the format: 128 has the bits 0x4300 and a last place
+// of 1, so 0x4300 | c is 128 + c, and minus 136 is exact. c - 8 and x are exact
+// bf16, so a group's products and their sum are plain fp32; the scale multiplies
+// the group's sum. The order of k inside a fragment is free as long as W and x
+// share it: nibbles i and i + 4 of a word are one register, and x is paired to
+// match.
 //
-// 16384 x 8192 weights, eight rows: 26.6 us, 2.6 TB/s of codes, scales and x.
-// By then the bound is the unpacking: eleven operations for eight codes, seven
-// of them on the integer pipe at half rate, which is 0.55 busy over the launch.
-// Four row tiles a warp (29 us), two or eight warps a block (31 us), six stages
-// (36 us) and x not loaded ahead (33 us) were slower. 64 rows: 96 us; 255
-// registers leave eight warps an SM, which wait for x and for their own results
-// (issue slots 31%, tensor pipe 38%). One row tile of W there was 128 us, two
-// blocks of 32 rows 110.
+// 16384 x 8192 weights, eight rows: 26.6 us (groups of 32: 38), 2.6 TB/s of codes,
+// scales and x. No unit is full there: integer pipe 46%, issue slots 50%, tensor
+// pipe 19%. 512 blocks of four warps, four an SM, are 0.86 of a wave: three
+// blocks on 80 of the SMs, so three or four warps a scheduler, each of which waits
+// for its own loads and its own sums in turn. Four row tiles a warp (29 us), two
+// or eight warps a block (31 us), six stages (36 us) and x not loaded ahead (33
+// us) were slower. 16 rows 41 us, 32 59, 64 92 to 96: 255 registers leave eight
+// warps an SM, which wait for x and for their own results (issue slots 30%, tensor
+// pipe 36%). One row tile of W for 64 rows was 128 us, two blocks of 32 rows 110.
 constexpr int kW4Stages = 4;
 constexpr int kW4Pitch = 80;        // bytes of a row in the ring: 64 and 16 against bank conflicts
 
@@ -245,7 +248,9 @@ struct QuantW4Args {
 // are taken with the rounded scale, the one that the product uses. A group of
 // zeros (or one whose scale rounds to zero) gets scale 1 and codes 8; a group
 // with a weight that is not finite gets scale NaN, so the product shows it.
-// E consecutive weights a lane, G / E lanes a group.
+// E consecutive weights a lane, G / E lanes a group. Loads of two bytes and stores
+// of one: 16384 x 8192 weights take 236 us in groups of 128 (64: 346, 32: 366),
+// the bytes alone 51; weights are laid out once.
 template <int G>
 __global__ void __launch_bounds__(256) quant_w4_kernel(const QuantW4Args a) {
     constexpr int E = G == 128 ? 4 : 2, L = G / E;
