@@ -92,21 +92,25 @@ def hstu_attn_workspace_bytes(B: int, total_tokens: int, max_seqlen: int, H: int
     return int(_lib().hstu_attn_workspace_bytes(B, total_tokens, max_seqlen, H, max(num_pos, 1)))
 
 
-@contextlib.contextmanager
+_CURRENT = contextlib.nullcontext(lambda t: t)
+
+
 def _allocating(stream):
     """Where a call on `stream` allocates. Another stream than the current one
     gets memory of its own: a block of the current stream's may still be in use
     there by queued work, although it was let go of. The current stream reads what
     goes through the given function (the results), so they are not handed out
     again before that is done."""
-    raw = None if stream is None else _stream(stream)
+    if stream is None:
+        return _CURRENT
+    raw, now = _stream(stream), torch.cuda.current_stream()
     if raw == 1:                        # cudaStreamLegacy: the default stream by another name
         raw = 0
-    now = None if raw is None else torch.cuda.current_stream()
-    if now is None or raw == now.cuda_stream:
-        yield lambda t: t
-        return
+    return _CURRENT if raw == now.cuda_stream else _elsewhere(raw, now)
 
+
+@contextlib.contextmanager
+def _elsewhere(raw: int, now):
     def result(t):
         t.record_stream(now)
         return t
