@@ -258,3 +258,27 @@ def test_thousands_of_new_tokens_in_a_row(dtype, d, H, ctx, new):
     tol = attn_tolerance(s, want, A, E)
     assert np.all(np.isfinite(got)) and np.all(np.abs(got - want) <= tol), \
         "off by up to %.3g times the bound" % np.max(np.abs(got - want) / tol)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 32), (BF, 64), (BF, 128), (F32, 32)])
+@pytest.mark.parametrize("ctx", [[50, 40, 30], [1500, 1100, 300]], ids=["short", "long"])
+@pytest.mark.parametrize("off", [[2, 12, 18, 26], [0, 10, 4, 12], [0, 10, 10, 40], [-3, 7, 13, 21]],
+                         ids=["begin", "fall", "end", "negative"])
+def test_offsets_that_cannot_be(dtype, d, ctx, off):
+    """Reported; rows that no sequence names stay as they were, rows that one
+    possible sequence names alone are its own."""
+    s = make_step(ctx, [10, 6, 8], "chain", 2, d, d, 16, dtype, seed=d + ctx[0])
+    T = 28
+    q, ts = torch.zeros(T, 2, d, dtype=dtype), np.full(T, 1_800_000_000, dtype=np.int64)
+    first = max(off[0], 0)
+    q[first: first + s.T], ts[first: first + s.T] = s.q, s.ts
+    out = torch.full((T, 2, d), 7.0, dtype=dtype).cuda()
+    call_attn(hstu, s, q=q.cuda(), timestamps=torch.from_numpy(ts).cuda(), max_new=10,
+              new_offsets=torch.tensor(off).cuda(), out=out)
+    assert hstu.hstu_device_status() == _native.HSTU_ERR_BAD_INPUT
+    named = np.zeros(T, dtype=bool)
+    for b in range(3):
+        named[max(off[b], 0): max(off[b + 1], 0)] = True
+    assert bool((out.cpu()[torch.from_numpy(~named)] == 7.0).all())
+    if off[0] == 0:             # sequence 0's first rows, before any other's
+        check_attn(s, out[: s.T], rows=slice(0, 4))
