@@ -192,3 +192,28 @@ def test_the_default_stream_given_while_another_is_current(name, handle):
         for r in (got, same):
             assert_same(name, tensors(r), want)
     assert hstu.hstu_device_status() == 0
+
+
+@pytest.mark.parametrize("name", [n for n in CALLS if n != "bias_indices"])     # (that one reads offsets)
+def test_a_side_stream_inside_a_capture(name):
+    """Allocations of a call on a stream that joined a capture, results let go of
+    inside it too; replayed twice."""
+    call, _ = CALLS[name](1)
+    want = tensors(call())
+    side = torch.cuda.Stream()
+    call(stream=side)                           # (first use outside)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        call(stream=side)
+        got = call(stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        copies = tensors(got)
+    for _ in range(2):
+        for t in copies:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert_same(name, copies, want)
+    assert hstu.hstu_device_status() == 0
